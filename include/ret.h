@@ -277,6 +277,90 @@ RET_API int ret_chunkwise_state_launches(int B, int H, int N, int dk, int dv, in
 RET_API ret_status ret_msr_norm_gate(const void* o, const void* gate, void* y, int B, int H, int N, int dv, float eps,
                                      ret_dtype dt, void* stream);
 
+/*
+ * Backward of ret_msr_norm_gate: gradients of sum(dy . y) with respect to o and gate. With
+ * r = 1 / sqrt(mean_c o^2 + eps), sig = 1 / (1 + exp(-gate)) and u = dy * gate * sig:
+ *   dout  = r u - o r^3 mean_c(u o),
+ *   dgate = dy * o r * (sig + gate * sig * (1 - sig)).
+ * o and dout [B, H, N, dv]; dy, gate and dgate token-major [B, N, H, dv]; all of dtype dt,
+ * sums fp32. One pass: each input is read once and each gradient written once. dout may be
+ * the o buffer, and dgate the gate or the dy buffer (in place); any other overlap of an
+ * output is rejected with RET_ERR_UNSUPPORTED. Other errors as ret_msr_norm_gate, and
+ * RET_ERR_ALIGN for a pointer that is not aligned to its element.
+ */
+RET_API ret_status ret_msr_norm_gate_backward(const void* dy, const void* o, const void* gate, void* dout, void* dgate,
+                                              int B, int H, int N, int dv, float eps, ret_dtype dt, void* stream);
+
+/* Where the two elements of a rotated pair lie in a head's first rot elements. */
+typedef enum {
+    RET_ROTARY_INTERLEAVED = 0, /* 2 i and 2 i + 1 */
+    RET_ROTARY_HALF = 1         /* i and i + rot / 2 */
+} ret_rotary_layout;
+
+/*
+ * Rotary prologue: queries and keys as the projections give them, rotated by their
+ * positions and written where retention reads them ([RM] 保留机制初识: RetNet's q and k
+ * carry the factors e^{i n theta} and e^{-i m theta}, so that a score depends on n - m).
+ * For the pair (a, b) at frequency i of a token at position p, with t = p * freqs[i]:
+ *   a' = s m (a cos t - b sin t),   b' = s m (a sin t + b cos t),
+ * m = amplitude, s = q_scale or k_scale; the d - rot elements behind the rotated part
+ * are multiplied by s. inverse != 0 takes -t: the gradient, and with m = s = 1 the inverse.
+ *   q, k          [B, N, Hq, d] and [B, N, Hk, d] of type dt, q_out and k_out likewise. Each
+ *                 has its own strides, in elements, of batch, token and head (a host array of
+ *                 three, read before the call returns); the d elements of a head are contiguous.
+ *                 Token-major projections (slices of a fused one too) and head-major
+ *                 retention operands are both views of this kind. Hk = 0: no k (k, k_out and
+ *                 their strides are not read).
+ *   freqs         [rot / 2] fp64, radians per position (rot = 0: NULL, the call only lays out
+ *                 and scales). The angle is formed in fp64: t keeps its digits at far positions.
+ *   p             offset + positions[b, n] if positions ([B, N] int64) is given, else
+ *                 offset + n, + starts[b] if starts ([B] int64) is given. Both: rejected.
+ * Arithmetic is fp32 (cos and sin within 2^-21), rounded once. An output may be its own input
+ * (same address and strides); an output that is not seen to be disjoint from the other
+ * tensors, or that writes an element twice, is rejected with RET_ERR_UNSUPPORTED. Column
+ * blocks of one row-strided buffer (same strides, heads at distinct places of a row) count as
+ * disjoint. RET_ERR_SHAPE: invalid sizes, rot odd or above d, a negative stride, a scale that
+ * is not finite. RET_ERR_ALIGN: a pointer not aligned to its element.
+ */
+RET_API ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, const long long* q_strides,
+                              const long long* k_strides, const long long* q_out_strides,
+                              const long long* k_out_strides, const double* freqs, const long long* positions,
+                              const long long* starts, long long offset, int B, int N, int Hq, int Hk, int d, int rot,
+                              ret_rotary_layout layout, int inverse, float amplitude, float q_scale, float k_scale,
+                              ret_dtype dt, void* stream);
+
+/*
+ * Layer norm of each of `rows` contiguous rows of D elements, the norm in front of a RetNet
+ * block's retention and feed-forward sub-layers:
+ *   s = x (+ residual),  y = weight * (s - mean_c s) / sqrt(mean_c (s - mean_c s)^2 + eps) + bias.
+ *   x, y          [rows, D] of type dt; residual and sum_out (s, rounded to dt) likewise, or NULL.
+ *   weight, bias  [D] of type wdt (dt or RET_F32), each or both NULL (1 and 0).
+ *   mean, rstd    [rows] fp32, the row statistics for the backward pass, or NULL.
+ * Statistics are fp32, of centred values, and with a residual of the unrounded sum. y and
+ * sum_out may each be the x or the residual buffer (in place); other overlaps of an output
+ * are rejected with RET_ERR_UNSUPPORTED. eps >= 0. rows = 0: nothing to do. RET_ERR_ALIGN: a pointer not
+ * aligned to its element.
+ */
+RET_API ret_status ret_layer_norm(const void* x, const void* residual, const void* weight, const void* bias, void* y,
+                                  void* sum_out, float* mean, float* rstd, long long rows, int D, float eps,
+                                  ret_dtype dt, ret_dtype wdt, void* stream);
+
+/*
+ * Backward of ret_layer_norm, from its statistics: with xh = (x - mean) rstd and u = weight * dy,
+ *   dx = rstd (u - mean_c u - xh mean_c(u xh)) (+ dsum),
+ *   dweight = sum_rows dy xh,   dbias = sum_rows dy.
+ * x is the normalised input: with a residual the forward's sum_out, and dx is then the gradient
+ * of x and of residual alike. dsum [rows, D]: the gradient that reaches sum_out by other ways, or NULL.
+ * dweight and dbias [D] of type wdt, each or both NULL; weight may be NULL (1). The sums over
+ * rows are fp32 and in a fixed order: calls with the same sizes on the same device agree bit for bit. dx may be the
+ * dy, x or dsum buffer (in place); other overlaps of an output are rejected with
+ * RET_ERR_UNSUPPORTED. May take stream-ordered scratch, freed on `stream` before the call
+ * returns. rows = 0: dweight and dbias receive zeros.
+ */
+RET_API ret_status ret_layer_norm_backward(const void* dy, const void* x, const void* weight, const float* mean,
+                                           const float* rstd, const void* dsum, void* dx, void* dweight, void* dbias,
+                                           long long rows, int D, ret_dtype dt, ret_dtype wdt, void* stream);
+
 /* Kernels one ret_chunkwise_backward (gated = 0) or gated_ret_chunkwise_backward
  * (gated = 1) call launches with these arguments, ddecay non-zero when the decay
  * gradient is requested (0 for an empty sequence, -1 if the arguments would be

@@ -159,4 +159,48 @@ norm_gate_scalar_kernel(const T* __restrict__ o, const T* gate, T* y, int H, int
     }
 }
 
+// Backward of the epilogue: with r = rsqrt(mean_c o^2 + eps), sig = 1 / (1 + e^-g) and
+// u = dy swish(g),
+//   do = r u - o r^3 mean_c (u o),   dg = dy o r (sig + swish(g) (1 - sig)).
+// sig as in swish() above.
+__device__ __forceinline__ float sigmoid(float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-x * kLog2e));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return r;
+}
+
+// Any dv and alignment: one warp per row, two passes over the row (the second from L1/L2).
+// dgate may be gate or dy, and dout o: an element is read by the thread that writes it.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads)
+norm_gate_backward_scalar_kernel(const T* dy, const T* o, const T* gate, T* dout, T* dgate, int H, int N, int dv,
+                                 float eps, size_t rows) {
+    const int lane = threadIdx.x & 31;
+    const size_t warps = (size_t)gridDim.x * (kNormThreads / 32);
+    for (size_t r = (size_t)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); r < rows; r += warps) {
+        size_t o_row, y_row;
+        norm_rows(r, H, N, o_row, y_row);
+        float ss = 0.f, uo = 0.f;
+        for (int c = lane; c < dv; c += 32) {
+            const float x = ld_elem(o + o_row * dv + c);
+            ss = fmaf(x, x, ss);
+            uo = fmaf(ld_elem(dy + y_row * dv + c) * swish(ld_elem(gate + y_row * dv + c)), x, uo);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            uo += __shfl_xor_sync(0xffffffffu, uo, off);
+        }
+        const float inv_rms = rsqrtf(ss / (float)dv + eps);
+        const float k = inv_rms * inv_rms * (uo / (float)dv);
+        for (int c = lane; c < dv; c += 32) {
+            const float x = ld_elem(o + o_row * dv + c), g = ld_elem(gate + y_row * dv + c);
+            const float d = ld_elem(dy + y_row * dv + c), sig = sigmoid(g);
+            st_elem(dout + o_row * dv + c, inv_rms * (d * (g * sig) - x * k));
+            st_elem(dgate + y_row * dv + c, d * (x * inv_rms) * (sig + g * sig * (1.f - sig)));
+        }
+    }
+}
+
 }  // namespace ret

@@ -1,6 +1,7 @@
 // C ABI of libret.so (declared in include/ret.h): host-side validation, kernel
 // selection and launch. One translation unit holds every kernel so that they
 // share the module-scope device error word.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -13,6 +14,8 @@
 #include "seqpar.cuh"
 #include "backward.cuh"
 #include "norm.cuh"
+#include "rotary.cuh"
+#include "layer_norm.cuh"
 
 using namespace ret;
 
@@ -480,6 +483,143 @@ inline bool ranges_overlap(const void* a, const void* b, size_t bytes) {
     return x < z + bytes && z < x + bytes;
 }
 
+// ------------------------------------------------------------------ rotary prologue (see rotary.cuh)
+
+// A strided [B, N, H, d] tensor: byte address, strides in elements, head dimension contiguous.
+struct Strided {
+    uintptr_t base;
+    long long st[3];  // batch, token, head
+    int n[3];
+    int d;
+    size_t elt;
+    // one past the last element, in elements from the base
+    long long extent() const {
+        long long e = d;
+        for (int i = 0; i < 3; ++i) e += st[i] * (long long)(n[i] - 1);
+        return e;
+    }
+    bool same(const Strided& o) const {
+        for (int i = 0; i < 3; ++i)
+            if (n[i] != o.n[i] || (n[i] > 1 && st[i] != o.st[i])) return false;
+        return base == o.base && d == o.d;
+    }
+};
+
+// No two indices of `v` share an element: taken by increasing stride, each dimension steps over all of the ones below it.
+bool writes_once(const Strided& v) {
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return v.st[a] < v.st[b]; });
+    long long span = v.d;
+    for (int i : order) {
+        if (v.n[i] == 1) continue;
+        if (v.st[i] < span) return false;
+        span += v.st[i] * (long long)(v.n[i] - 1);
+    }
+    return true;
+}
+
+// Whether a and b are seen to share no element: their address ranges are disjoint, or they are
+// column blocks of one row-strided buffer (slices of a fused projection): the same row stride,
+// and heads at distinct places of each row.
+bool disjoint(const Strided& a, const Strided& b) {
+    const uintptr_t ea = a.base + (uintptr_t)a.extent() * a.elt, eb = b.base + (uintptr_t)b.extent() * b.elt;
+    if (ea <= b.base || eb <= a.base) return true;
+    long long row = 0;  // the stride of rows; batches of both must be whole rows apart
+    for (int i = 1; i >= 0; --i) {
+        if (a.n[i] == 1 && b.n[i] == 1) continue;
+        const long long s = a.n[i] > 1 ? a.st[i] : b.st[i];
+        if ((a.n[i] > 1 && a.st[i] != s) || (b.n[i] > 1 && b.st[i] != s)) return false;
+        if (row == 0) row = s;
+        else if (s % row != 0) return false;
+    }
+    const long long bytes = (long long)(b.base - a.base), elt = (long long)a.elt;
+    if (row <= 0 || bytes % elt != 0) return false;
+    const long long wa = a.st[2] * (a.n[2] - 1) + a.d, wb = b.st[2] * (b.n[2] - 1) + b.d;
+    const long long at = ((bytes / elt) % row + row) % row;
+    return at >= wa && at + wb <= row;
+}
+
+template <typename T>
+ret_status launch_rotary(const RotArgs& a, bool half, cudaStream_t st) {
+    const size_t total = (size_t)a.B * a.N * (a.x[0].H + a.x[1].H) * (size_t)(a.d - a.rot / 2);
+    const unsigned grid = (unsigned)std::min<size_t>((total + kRotThreads - 1) / kRotThreads, (size_t)32 * tc::sm_count());
+    if (half)
+        rotary_kernel<T, true><<<grid, kRotThreads, 0, st>>>(a, total);
+    else
+        rotary_kernel<T, false><<<grid, kRotThreads, 0, st>>>(a, total);
+    return launch_status();
+}
+
+// ------------------------------------------------------------------ layer norm (see layer_norm.cuh)
+
+inline unsigned block_rows(long long rows) {
+    return (unsigned)std::min<long long>(rows, (long long)32 * tc::sm_count());
+}
+
+template <typename T, typename W>
+ret_status launch_layer_norm(const void* x, const void* res, const void* w, const void* b, void* y, void* sum_out,
+                             float* mean, float* rstd, long long rows, int D, float eps, cudaStream_t st) {
+    ln_forward_rows_kernel<T, W><<<block_rows(rows), kLnThreads, 0, st>>>(
+        static_cast<const T*>(x), static_cast<const T*>(res), static_cast<const W*>(w), static_cast<const W*>(b),
+        static_cast<T*>(y), static_cast<T*>(sum_out), mean, rstd, (size_t)rows, D, eps);
+    return launch_status();
+}
+
+template <typename T, typename W>
+ret_status launch_layer_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
+                                      const float* rstd, const void* dsum, void* dx, void* dw, void* db,
+                                      long long rows, int D, cudaStream_t st) {
+    const T* dyp = static_cast<const T*>(dy);
+    const T* xp = static_cast<const T*>(x);
+    ret_status r = RET_OK;
+    if (dw || db) {
+        const unsigned cols = (unsigned)((D + kLnThreads - 1) / kLnThreads);
+        const unsigned parts = (unsigned)std::min<long long>(rows, std::max(1u, 8u * tc::sm_count() / cols));
+        tc::keep_pool_memory();
+        float* part = nullptr;
+        if (cudaMallocAsync(reinterpret_cast<void**>(&part), sizeof(float) * 2 * (size_t)parts * D, st) != cudaSuccess)
+            return RET_ERR_CUDA;
+        ln_backward_columns_kernel<T><<<dim3(cols, parts), kLnThreads, 0, st>>>(dyp, xp, mean, rstd, part, (size_t)rows,
+                                                                               D);
+        r = launch_status();
+        if (r == RET_OK) {
+            ln_reduce_kernel<W><<<cols, kLnThreads, 0, st>>>(part, (int)parts, static_cast<W*>(dw),
+                                                             static_cast<W*>(db), D);
+            r = launch_status();
+        }
+        if (cudaFreeAsync(part, st) != cudaSuccess && r == RET_OK) r = RET_ERR_CUDA;
+        if (r != RET_OK) return r;
+    }
+    // last: dx may take dy's place
+    ln_backward_rows_kernel<T, W><<<block_rows(rows), kLnThreads, 0, st>>>(
+        dyp, xp, static_cast<const W*>(w), mean, rstd, static_cast<const T*>(dsum), static_cast<T*>(dx), (size_t)rows,
+        D);
+    return launch_status();
+}
+
+template <typename T>
+ret_status launch_norm_gate_backward(const void* dy, const void* o, const void* gate, void* dout, void* dgate, int B,
+                                     int H, int N, int dv, float eps, cudaStream_t st) {
+    const size_t rows = (size_t)B * N * H;
+    const size_t blocks = std::min<size_t>((rows + kNormThreads / 32 - 1) / (kNormThreads / 32),
+                                           (size_t)32 * tc::sm_count());
+    norm_gate_backward_scalar_kernel<T><<<(unsigned)blocks, kNormThreads, 0, st>>>(
+        static_cast<const T*>(dy), static_cast<const T*>(o), static_cast<const T*>(gate), static_cast<T*>(dout),
+        static_cast<T*>(dgate), H, N, dv, eps, rows);
+    return launch_status();
+}
+
+constexpr long long kMaxElements = 1LL << 46;  // of one tensor: more than any device holds, so that byte counts fit
+inline size_t elt_size(ret_dtype dt) { return dt == RET_BF16 ? 2 : 4; }
+inline bool valid_dtype(int dt) { return dt == RET_F32 || dt == RET_BF16; }
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte; a null pointer shares none.
+inline bool bytes_overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), z = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < z + nb && z < x + na;
+}
+
 template <typename T>
 ret_status launch_parallel(const void* q, const void* k, const void* v, const float* gamma, void* o,
                            int B, int H, int N, int dk, int dv, cudaStream_t st) {
@@ -938,6 +1078,167 @@ ret_status ret_msr_norm_gate(const void* o, const void* gate, void* y, int B, in
     cudaStream_t st = as_stream(stream);
     if (dt == RET_BF16) return launch_norm_gate<__nv_bfloat16>(o, gate, y, B, H, N, dv, eps, st);
     return launch_norm_gate<float>(o, gate, y, B, H, N, dv, eps, st);
+}
+
+ret_status ret_msr_norm_gate_backward(const void* dy, const void* o, const void* gate, void* dout, void* dgate, int B,
+                                      int H, int N, int dv, float eps, ret_dtype dt, void* stream) {
+    if (!valid_dtype(dt)) return RET_ERR_DTYPE;
+    if (B <= 0 || H <= 0 || N < 0 || dv <= 0) return RET_ERR_SHAPE;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return RET_ERR_SHAPE;
+    if (N == 0) return RET_OK;
+    if (!dy || !o || !gate || !dout || !dgate) return RET_ERR_NULL;
+    const size_t bytes = (size_t)B * H * N * dv * elt_size(dt);
+    for (const void* p : {dy, o, gate, static_cast<const void*>(dout), static_cast<const void*>(dgate)})
+        if (!aligned_to(p, elt_size(dt))) return RET_ERR_ALIGN;
+    // dout may take o's place, dgate that of gate or dy; any other overlap would race
+    if (ranges_overlap(dout, dgate, bytes) || ranges_overlap(dout, gate, bytes) || ranges_overlap(dout, dy, bytes) ||
+        (dout != o && ranges_overlap(dout, o, bytes)) || ranges_overlap(dgate, o, bytes) ||
+        (dgate != gate && ranges_overlap(dgate, gate, bytes)) || (dgate != dy && ranges_overlap(dgate, dy, bytes)))
+        return RET_ERR_UNSUPPORTED;
+    cudaStream_t st = as_stream(stream);
+    if (dt == RET_BF16) return launch_norm_gate_backward<__nv_bfloat16>(dy, o, gate, dout, dgate, B, H, N, dv, eps, st);
+    return launch_norm_gate_backward<float>(dy, o, gate, dout, dgate, B, H, N, dv, eps, st);
+}
+
+ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, const long long* q_strides,
+                      const long long* k_strides, const long long* q_out_strides, const long long* k_out_strides,
+                      const double* freqs, const long long* positions, const long long* starts, long long offset,
+                      int B, int N, int Hq, int Hk, int d, int rot, ret_rotary_layout layout, int inverse,
+                      float amplitude, float q_scale, float k_scale, ret_dtype dt, void* stream) {
+    if (!valid_dtype(dt)) return RET_ERR_DTYPE;
+    if (B <= 0 || N < 0 || Hq <= 0 || Hk < 0 || d <= 0 || rot < 0 || rot > d || rot % 2 != 0) return RET_ERR_SHAPE;
+    if (!std::isfinite(amplitude) || !std::isfinite(q_scale) || !std::isfinite(k_scale)) return RET_ERR_SHAPE;
+    if (layout != RET_ROTARY_INTERLEAVED && layout != RET_ROTARY_HALF) return RET_ERR_UNSUPPORTED;
+    if (N == 0) return RET_OK;
+    if (!q || !q_out || !q_strides || !q_out_strides || (rot > 0 && !freqs)) return RET_ERR_NULL;
+    if (Hk > 0 && (!k || !k_out || !k_strides || !k_out_strides)) return RET_ERR_NULL;
+    if (positions && starts) return RET_ERR_UNSUPPORTED;
+    const size_t elt = elt_size(dt);
+    RotArgs a{};
+    Strided in[2], out[2];
+    const void* src[2] = {q, k};
+    void* dst[2] = {q_out, k_out};
+    const long long* ss[2] = {q_strides, k_strides};
+    const long long* ds[2] = {q_out_strides, k_out_strides};
+    const int heads[2] = {Hq, Hk}, T = Hk > 0 ? 2 : 1;
+    const float scale[2] = {q_scale, k_scale};
+    const size_t tokens = (size_t)B * N;
+    for (int t = 0; t < T; ++t) {
+        for (int i = 0; i < 3; ++i)
+            if (ss[t][i] < 0 || ds[t][i] < 0) return RET_ERR_SHAPE;
+        if (!aligned_to(src[t], elt) || !aligned_to(dst[t], elt)) return RET_ERR_ALIGN;
+        for (const long long* x : {ss[t], ds[t]})
+            if ((__int128)x[0] * B + (__int128)x[1] * N + (__int128)x[2] * heads[t] + d > kMaxElements)
+                return RET_ERR_UNSUPPORTED;
+        in[t] = {reinterpret_cast<uintptr_t>(src[t]), {ss[t][0], ss[t][1], ss[t][2]}, {B, N, heads[t]}, d, elt};
+        out[t] = {reinterpret_cast<uintptr_t>(dst[t]), {ds[t][0], ds[t][1], ds[t][2]}, {B, N, heads[t]}, d, elt};
+        a.x[t] = {src[t], dst[t], ss[t][0], ss[t][1], ss[t][2], ds[t][0], ds[t][1], ds[t][2], heads[t], scale[t]};
+    }
+    // each output element is written once and read by nobody else; an output may be its own input
+    for (int t = 0; t < T; ++t) {
+        if (!writes_once(out[t])) return RET_ERR_UNSUPPORTED;
+        const size_t bytes = (size_t)out[t].extent() * elt;
+        if (bytes_overlap(dst[t], bytes, freqs, sizeof(double) * (size_t)(rot / 2)) ||
+            bytes_overlap(dst[t], bytes, positions, 8 * tokens) || bytes_overlap(dst[t], bytes, starts, 8 * (size_t)B))
+            return RET_ERR_UNSUPPORTED;
+        for (int i = 0; i < T; ++i)
+            if (!disjoint(out[t], in[i]) && !(i == t && out[t].same(in[t]))) return RET_ERR_UNSUPPORTED;
+    }
+    if (T == 2 && !disjoint(out[0], out[1])) return RET_ERR_UNSUPPORTED;
+    a.freqs = freqs;
+    a.positions = positions;
+    a.starts = starts;
+    a.offset = offset;
+    a.B = B;
+    a.N = N;
+    a.d = d;
+    a.rot = rot;
+    a.amplitude = amplitude;
+    a.sign = inverse ? -1.f : 1.f;
+    cudaStream_t st = as_stream(stream);
+    if (dt == RET_BF16) return launch_rotary<__nv_bfloat16>(a, layout == RET_ROTARY_HALF, st);
+    return launch_rotary<float>(a, layout == RET_ROTARY_HALF, st);
+}
+
+ret_status ret_layer_norm(const void* x, const void* residual, const void* weight, const void* bias, void* y,
+                          void* sum_out, float* mean, float* rstd, long long rows, int D, float eps, ret_dtype dt,
+                          ret_dtype wdt, void* stream) {
+    if (!valid_dtype(dt) || !valid_dtype(wdt)) return RET_ERR_DTYPE;
+    if (wdt != dt && wdt != RET_F32) return RET_ERR_DTYPE;
+    if (rows < 0 || D <= 0) return RET_ERR_SHAPE;
+    if (rows > kMaxElements / D) return RET_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return RET_ERR_SHAPE;
+    if (rows == 0) return RET_OK;
+    if (!x || !y) return RET_ERR_NULL;
+    const size_t elt = elt_size(dt), welt = elt_size(wdt);
+    if (!aligned_to(x, elt) || !aligned_to(residual, elt) || !aligned_to(y, elt) || !aligned_to(sum_out, elt) ||
+        !aligned_to(weight, welt) || !aligned_to(bias, welt) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+        return RET_ERR_ALIGN;
+    // y and sum_out may each take the place of x or residual; any other overlap would race
+    const size_t bytes = (size_t)rows * D * elt, wb = (size_t)D * welt, sb = (size_t)rows * 4;
+    for (const void* out : {static_cast<const void*>(y), static_cast<const void*>(sum_out)}) {
+        if ((out != x && bytes_overlap(out, bytes, x, bytes)) ||
+            (out != residual && bytes_overlap(out, bytes, residual, bytes)) || bytes_overlap(out, bytes, weight, wb) ||
+            bytes_overlap(out, bytes, bias, wb) || bytes_overlap(out, bytes, mean, sb) ||
+            bytes_overlap(out, bytes, rstd, sb))
+            return RET_ERR_UNSUPPORTED;
+    }
+    if (bytes_overlap(y, bytes, sum_out, bytes) || bytes_overlap(mean, sb, rstd, sb)) return RET_ERR_UNSUPPORTED;
+    for (const void* stat : {static_cast<const void*>(mean), static_cast<const void*>(rstd)})
+        if (bytes_overlap(stat, sb, x, bytes) || bytes_overlap(stat, sb, residual, bytes) ||
+            bytes_overlap(stat, sb, weight, wb) || bytes_overlap(stat, sb, bias, wb))
+            return RET_ERR_UNSUPPORTED;
+    cudaStream_t st = as_stream(stream);
+    if (dt == RET_F32)
+        return launch_layer_norm<float, float>(x, residual, weight, bias, y, sum_out, mean, rstd, rows, D, eps, st);
+    if (wdt == RET_F32)
+        return launch_layer_norm<__nv_bfloat16, float>(x, residual, weight, bias, y, sum_out, mean, rstd, rows, D, eps,
+                                                       st);
+    return launch_layer_norm<__nv_bfloat16, __nv_bfloat16>(x, residual, weight, bias, y, sum_out, mean, rstd, rows, D,
+                                                           eps, st);
+}
+
+ret_status ret_layer_norm_backward(const void* dy, const void* x, const void* weight, const float* mean,
+                                   const float* rstd, const void* dsum, void* dx, void* dweight, void* dbias,
+                                   long long rows, int D, ret_dtype dt, ret_dtype wdt, void* stream) {
+    if (!valid_dtype(dt) || !valid_dtype(wdt)) return RET_ERR_DTYPE;
+    if (wdt != dt && wdt != RET_F32) return RET_ERR_DTYPE;
+    if (rows < 0 || D <= 0) return RET_ERR_SHAPE;
+    if (rows > kMaxElements / D) return RET_ERR_UNSUPPORTED;
+    cudaStream_t st = as_stream(stream);
+    const size_t elt = elt_size(dt), welt = elt_size(wdt);
+    const size_t bytes = (size_t)rows * D * elt, wb = (size_t)D * welt, sb = (size_t)rows * 4;
+    if (rows == 0) {  // sums over no rows
+        for (void* p : {dweight, dbias})
+            if (p && cudaMemsetAsync(p, 0, wb, st) != cudaSuccess) return RET_ERR_CUDA;
+        return RET_OK;
+    }
+    if (!dy || !x || !mean || !rstd || !dx) return RET_ERR_NULL;
+    if (!aligned_to(dy, elt) || !aligned_to(x, elt) || !aligned_to(dsum, elt) || !aligned_to(dx, elt) ||
+        !aligned_to(weight, welt) || !aligned_to(dweight, welt) || !aligned_to(dbias, welt) || !aligned_to(mean, 4) ||
+        !aligned_to(rstd, 4))
+        return RET_ERR_ALIGN;
+    // dx may take the place of dy, x or dsum; any other overlap would race
+    for (const void* in : {dy, x, dsum})
+        if ((in != dx && bytes_overlap(dx, bytes, in, bytes)) || bytes_overlap(dweight, wb, in, bytes) ||
+            bytes_overlap(dbias, wb, in, bytes))
+            return RET_ERR_UNSUPPORTED;
+    const struct { const void* p; size_t n; } outs[] = {{dx, bytes}, {dweight, wb}, {dbias, wb}};
+    for (const auto& o : outs)
+        if (bytes_overlap(o.p, o.n, weight, wb) || bytes_overlap(o.p, o.n, mean, sb) ||
+            bytes_overlap(o.p, o.n, rstd, sb))
+            return RET_ERR_UNSUPPORTED;
+    if (bytes_overlap(dx, bytes, dweight, wb) || bytes_overlap(dx, bytes, dbias, wb) ||
+        bytes_overlap(dweight, wb, dbias, wb))
+        return RET_ERR_UNSUPPORTED;
+    if (dt == RET_F32)
+        return launch_layer_norm_backward<float, float>(dy, x, weight, mean, rstd, dsum, dx, dweight, dbias, rows, D,
+                                                        st);
+    if (wdt == RET_F32)
+        return launch_layer_norm_backward<__nv_bfloat16, float>(dy, x, weight, mean, rstd, dsum, dx, dweight, dbias,
+                                                                rows, D, st);
+    return launch_layer_norm_backward<__nv_bfloat16, __nv_bfloat16>(dy, x, weight, mean, rstd, dsum, dx, dweight,
+                                                                    dbias, rows, D, st);
 }
 
 int ret_chunkwise_backward_launches(int B, int H, int N, int dk, int dv, int chunk, ret_dtype dt, int gated,

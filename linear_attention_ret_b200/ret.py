@@ -12,6 +12,7 @@ state [B, H, dk, dv] fp32. q, k, v share one dtype (float32 or bfloat16).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -31,13 +32,16 @@ SYMBOLS = ("ret_parallel", "ret_chunkwise", "ret_recurrent_step", "gated_ret_chu
            "ret_chunkwise_state", "gated_ret_chunkwise_state", "ret_state_prefix", "ret_chunkwise_state_launches",
            "ret_chunkwise_backward", "gated_ret_chunkwise_backward", "ret_chunkwise_backward_launches",
            "ret_msr_norm_gate", "ret_chunkwise_noalloc_scratch_bytes", "ret_chunkwise_host",
-           "gated_ret_chunkwise_host", "ret_chunkwise_backward_host", "gated_ret_chunkwise_backward_host")
+           "gated_ret_chunkwise_host", "ret_chunkwise_backward_host", "gated_ret_chunkwise_backward_host",
+           "ret_msr_norm_gate_backward", "ret_rotary", "ret_layer_norm", "ret_layer_norm_backward")
 
 _lock = threading.Lock()
 _lib = None
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
+_f = ctypes.c_float
 
 
 class RetError(RuntimeError):
@@ -73,6 +77,12 @@ def load(path: str | None = None) -> ctypes.CDLL:
             getattr(lib, fn).restype = _i
         lib.ret_msr_norm_gate.argtypes = [_vp, _vp, _vp, _i, _i, _i, _i, ctypes.c_float, _i, _vp]
         lib.ret_msr_norm_gate.restype = _i
+        lib.ret_msr_norm_gate_backward.argtypes = [_vp] * 5 + [_i] * 4 + [_f, _i, _vp]
+        lib.ret_rotary.argtypes = [_vp] * 11 + [_ll] + [_i] * 8 + [_f] * 3 + [_i, _vp]
+        lib.ret_layer_norm.argtypes = [_vp] * 8 + [_ll, _i, _f, _i, _i, _vp]
+        lib.ret_layer_norm_backward.argtypes = [_vp] * 9 + [_ll, _i, _i, _i, _vp]
+        for fn in ("ret_msr_norm_gate_backward", "ret_rotary", "ret_layer_norm", "ret_layer_norm_backward"):
+            getattr(lib, fn).restype = _i
         for fn in ("ret_chunkwise_backward", "gated_ret_chunkwise_backward", "ret_chunkwise_backward_host",
                    "gated_ret_chunkwise_backward_host"):
             getattr(lib, fn).argtypes = [_vp] * 9 + [_i] * 7 + [_vp]
@@ -372,6 +382,195 @@ def msr_norm_gate(o, gate, eps: float = 1e-5, y=None, stream=None):
     _check("ret_msr_norm_gate", load().ret_msr_norm_gate(_ptr(o), _ptr(gate), _ptr(y), B, H, N, dv, float(eps), _dt(o),
                                                          _stream(stream)))
     return y
+
+
+@contextlib.contextmanager
+def _launching(device, stream):
+    """The tensors' device is current inside and `stream` (None: that device's current stream) is
+    the one that outputs are allocated and the call is enqueued on; yields its handle."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
+        with torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def msr_norm_gate_backward(dy, o, gate, eps: float = 1e-5, dout=None, dgate=None, stream=None):
+    """Gradients of sum(dy * msr_norm_gate(o, gate, eps)). dy, gate [B, N, H, dv]; o [B, H, N, dv].
+    Returns (dout [B, H, N, dv], dgate [B, N, H, dv]); dout may be o, dgate may be gate or dy."""
+    _rank("o", o, 4)
+    B, H, N, dv = o.shape
+    for name, t, shape in (("gate", gate, (B, N, H, dv)), ("dy", dy, (B, N, H, dv)), ("dout", dout, (B, H, N, dv)),
+                           ("dgate", dgate, (B, N, H, dv))):
+        _expect(name, t, shape, o.dtype)
+    dt = _dt(o)
+    _cuda(o, gate, dy, dout, dgate)
+    with _launching(o.device, stream) as s:
+        dout = torch.empty_like(o) if dout is None else dout
+        dgate = torch.empty_like(gate) if dgate is None else dgate
+        _check("ret_msr_norm_gate_backward",
+               load().ret_msr_norm_gate_backward(_ptr(dy), _ptr(o), _ptr(gate), _ptr(dout), _ptr(dgate), B, H, N, dv,
+                                                 float(eps), dt, s))
+    return dout, dgate
+
+
+ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}  # ret_rotary_layout in include/ret.h
+
+
+def _rotate(q, k, q_out, k_out, freqs, positions, starts, offset, layout, inverse, amplitude, q_scale, k_scale,
+            stream):
+    """One ret_rotary call. Token-major [B, N, H, d] in and head-major [B, H, N, d] out, or with
+    inverse the other way round. Outputs that are None are allocated contiguous."""
+    for name, t in (("q", q), ("k", k), ("the output of q", q_out), ("the output of k", k_out)):
+        if t is not None:
+            _rank(name, t, 4)
+
+    def token_major(t, given):
+        return t.transpose(1, 2) if t is not None and given == inverse else t
+
+    B, N, Hq, d = token_major(q, True).shape
+    Hk = 0 if k is None else token_major(k, True).shape[2]
+    if k is None and k_out is not None:
+        raise ValueError("an output for k was given without k")
+    _expect("k", k, (B, Hk, N, d) if inverse else (B, N, Hk, d), q.dtype)
+    _expect("the output of q", q_out, (B, N, Hq, d) if inverse else (B, Hq, N, d), q.dtype)
+    _expect("the output of k", k_out, (B, N, Hk, d) if inverse else (B, Hk, N, d), q.dtype)
+    rot = 0
+    if freqs is not None:
+        _rank("freqs", freqs, 1)
+        rot = 2 * freqs.shape[0]
+        _expect("freqs", freqs, freqs.shape, torch.float64)
+        if rot > d:
+            raise ValueError(f"freqs rotates {rot} elements of a head of {d}")
+    if positions is not None and starts is not None:
+        raise ValueError("give positions or starts, not both")
+    _expect("positions", positions, (B, N), torch.int64)
+    _expect("starts", starts, (B,), torch.int64)
+    if layout not in ROTARY_LAYOUTS:
+        raise ValueError(f"layout must be one of {tuple(ROTARY_LAYOUTS)}, got {layout!r}")
+    dt = _dt(q)
+    for name, t in (("q", q), ("k", k), ("the output of q", q_out), ("the output of k", k_out)):
+        if t is not None and d > 1 and t.stride(3) != 1:
+            raise ValueError(f"the head dimension of {name} must be contiguous")
+    _cuda(freqs, positions, starts)
+    for t in (q, k, q_out, k_out, freqs, positions, starts):
+        if t is not None and (not t.is_cuda or t.device != q.device):
+            raise ValueError(f"tensors must be CUDA tensors on one device, got {q.device} and {t.device}")
+    with _launching(q.device, stream) as s:
+        def out(t, heads):
+            if t is not None:
+                return t
+            return torch.empty((B, N, heads, d) if inverse else (B, heads, N, d), dtype=q.dtype, device=q.device)
+
+        q_out, k_out = out(q_out, Hq), None if k is None else out(k_out, Hk)
+        views = [token_major(t, given) for t, given in ((q, True), (k, True), (q_out, False), (k_out, False))]
+        strides = [None if t is None else (_ll * 3)(*t.stride()[:3]) for t in views]
+        _check("ret_rotary",
+               load().ret_rotary(*(_ptr(t) for t in views), *strides, _ptr(freqs), _ptr(positions), _ptr(starts),
+                                 int(offset), B, N, Hq, Hk, d, rot, ROTARY_LAYOUTS[layout], int(inverse),
+                                 float(amplitude), float(q_scale), float(k_scale), dt, s))
+    return q_out, k_out
+
+
+def rotary(q, k, freqs, positions=None, starts=None, offset=0, layout="interleaved", amplitude=1.0, q_scale=1.0,
+           k_scale=1.0, q_out=None, k_out=None, stream=None):
+    """Rotary prologue: q [B, N, Hq, d] and k [B, N, Hk, d] (or None) as the projections give them,
+    rotated by their positions and laid out head-major for the retention calls. Returns
+    (q_out [B, Hq, N, d], k_out [B, Hk, N, d] or None).
+
+    q and k may be any strided views whose head dimension is contiguous (slices of a fused
+    projection), q_out and k_out too; an output may be its own input (q_out=q.transpose(1, 2)).
+    freqs [rot / 2] fp64 is radians per position of each pair (rotary.frequencies makes it), None
+    for a call that only lays out and scales. The position of token n is offset + positions[b, n],
+    or offset + n (+ starts[b]); positions [B, N] and starts [B] are int64. layout: "interleaved"
+    pairs (2i, 2i+1) or "half" pairs (i, i + rot/2). The rotated part is multiplied by amplitude,
+    the whole head by q_scale or k_scale."""
+    return _rotate(q, k, q_out, k_out, freqs, positions, starts, offset, layout, False, amplitude, q_scale, k_scale,
+                   stream)
+
+
+def rotary_backward(dq, dk, freqs, positions=None, starts=None, offset=0, layout="interleaved", amplitude=1.0,
+                    q_scale=1.0, k_scale=1.0, dq_out=None, dk_out=None, stream=None):
+    """Gradient of rotary: dq [B, Hq, N, d] and dk [B, Hk, N, d] (or None), as the retention backward
+    gives them, to token-major (dq_out [B, N, Hq, d], dk_out [B, N, Hk, d] or None). Arguments as
+    rotary; with amplitude and scales 1 it is also its inverse."""
+    return _rotate(dq, dk, dq_out, dk_out, freqs, positions, starts, offset, layout, True, amplitude, q_scale, k_scale,
+                   stream)
+
+
+def _norm_args(x, weight, bias):
+    """x [..., D]; weight and bias [D] of x's dtype or fp32, each or both None. Returns (rows, D, weight dtype)."""
+    if x.dim() == 0:
+        raise ValueError("x must have at least one dimension")
+    D = x.shape[-1]
+    if D == 0:
+        raise ValueError(f"x must have rows of at least one element, got shape {tuple(x.shape)}")
+    _expect("weight", weight, (D,))
+    _expect("bias", bias, (D,))
+    w = weight if weight is not None else bias
+    if w is not None and w.dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"weight and bias must be {x.dtype} or torch.float32, got {w.dtype}")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise ValueError(f"weight and bias must share one dtype, got {weight.dtype} and {bias.dtype}")
+    return x.numel() // D, D, x.dtype if w is None else w.dtype
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, y=None, sum_out=None, mean=None,
+               rstd=None, stream=None):
+    """Layer norm over the last dimension of x [..., D], with weight and bias [D] (x's dtype or fp32, or
+    None). Returns y. With a residual (x's shape and dtype) it normalises x + residual and returns
+    (y, sum_out). mean and rstd (fp32, x's shape without D) receive the row statistics for
+    layer_norm_backward if given. y and sum_out may each be the x or the residual tensor."""
+    rows, D, wdtype = _norm_args(x, weight, bias)
+    for name, t in (("residual", residual), ("y", y), ("sum_out", sum_out)):
+        _expect(name, t, x.shape, x.dtype)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _expect(name, t, x.shape[:-1], torch.float32)
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out was given without a residual")
+    dt = _dt(x)
+    _cuda(x, weight, bias, residual, y, sum_out, mean, rstd)
+    with _launching(x.device, stream) as s:
+        y = torch.empty_like(x) if y is None else y
+        if residual is not None and sum_out is None:
+            sum_out = torch.empty_like(x)
+        _check("ret_layer_norm",
+               load().ret_layer_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(y), _ptr(sum_out),
+                                     _ptr(mean), _ptr(rstd), rows, D, float(eps), dt,
+                                     RET_BF16 if wdtype == torch.bfloat16 else RET_F32, s))
+    return y if residual is None else (y, sum_out)
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, dsum=None, dweight=True, dbias=True, wdtype=None, dx=None,
+                        stream=None):
+    """Gradients of layer_norm from its statistics. x is the tensor that was normalised (with a residual,
+    the forward's sum_out); dsum (x's shape) the gradient that reaches that sum by other ways, added to
+    dx. Returns (dx, dweight, dbias), dweight None without a weight or with dweight=False, dbias None
+    without dbias. dx may be the dy, x or dsum tensor. The dtype of dbias is the weight's, or wdtype
+    (x's) where there is no weight."""
+    rows, D, wd = _norm_args(x, weight, None)
+    if weight is None and wdtype is not None:
+        if wdtype not in (x.dtype, torch.float32):
+            raise ValueError(f"wdtype must be {x.dtype} or torch.float32, got {wdtype}")
+        wd = wdtype
+    for name, t in (("dy", dy), ("dsum", dsum), ("dx", dx)):
+        _expect(name, t, x.shape, x.dtype)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _expect(name, t, x.shape[:-1], torch.float32)
+    dt = _dt(x)
+    _cuda(dy, x, weight, mean, rstd, dsum, dx)
+    with _launching(x.device, stream) as s:
+        dx = torch.empty_like(x) if dx is None else dx
+        dw = torch.empty(D, dtype=wd, device=x.device) if dweight and weight is not None else None
+        db = torch.empty(D, dtype=wd, device=x.device) if dbias else None
+        _check("ret_layer_norm_backward",
+               load().ret_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dsum),
+                                              _ptr(dx), _ptr(dw), _ptr(db), rows, D, dt,
+                                              RET_BF16 if wd == torch.bfloat16 else RET_F32, s))
+    return dx, dw, db
 
 
 def last_device_error(stream=None) -> int:
