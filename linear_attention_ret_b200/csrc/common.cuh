@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "ret.h"
 
@@ -35,6 +36,57 @@ template <typename T>
 __device__ __forceinline__ float ld_elem(const T* p) { return Elem<T>::load(p); }
 template <typename T>
 __device__ __forceinline__ void st_elem(T* p, float x) { Elem<T>::store(p, x); }
+
+// VE consecutive elements moved as one access of VE * sizeof(T) bytes (2, 4, 8 or 16), the
+// address a multiple of that. load_cs evicts first: for tensors that are read once.
+template <int BYTES> struct RawBytes;
+template <> struct RawBytes<2> { using type = unsigned short; };
+template <> struct RawBytes<4> { using type = unsigned int; };
+template <> struct RawBytes<8> { using type = uint2; };
+template <> struct RawBytes<16> { using type = uint4; };
+
+template <typename T, int VE>
+struct Vec {
+    using Raw = typename RawBytes<VE * (int)sizeof(T)>::type;
+    static __device__ __forceinline__ Raw load_cs(const T* p) { return __ldcs(reinterpret_cast<const Raw*>(p)); }
+    static __device__ __forceinline__ Raw load(const T* p) { return *reinterpret_cast<const Raw*>(p); }
+    static __device__ __forceinline__ Raw zero() {
+        Raw r;
+        memset(&r, 0, sizeof(r));
+        return r;
+    }
+    static __device__ __forceinline__ void unpack(const Raw& u, float* f) {
+        T e[VE];
+        memcpy(e, &u, sizeof(u));
+#pragma unroll
+        for (int i = 0; i < VE; ++i) f[i] = ld_elem(e + i);
+    }
+    static __device__ __forceinline__ void store(T* p, const float* f) {
+        T e[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) st_elem(e + i, f[i]);
+        Raw r;
+        memcpy(&r, e, sizeof(r));
+        *reinterpret_cast<Raw*>(p) = r;
+    }
+};
+
+// Division of a 32-bit number by a fixed 32-bit d >= 1, exact for every n < 2^31: with
+// l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (umulhi(m, n) + n) >> l
+// (Granlund and Montgomery, Division by invariant integers using multiplication, 1994).
+struct FastDiv {
+    unsigned d, m, l;
+    FastDiv() = default;
+    explicit FastDiv(unsigned d_) : d(d_), l(0) {
+        while ((1ull << l) < d) ++l;
+        m = (unsigned)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+    }
+    __device__ __forceinline__ unsigned div(unsigned n) const { return (__umulhi(m, n) + n) >> l; }
+    __device__ __forceinline__ void divmod(unsigned n, unsigned& q, unsigned& r) const {
+        q = div(n);
+        r = n - q * d;
+    }
+};
 
 // gamma^n for an integer n >= 0 given log2(gamma); gamma^0 = 1 even for gamma = 0
 // (log2(0) = -inf and exp2(-inf) = 0 give the n > 0 cases).

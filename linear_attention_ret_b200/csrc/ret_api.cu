@@ -539,14 +539,56 @@ bool disjoint(const Strided& a, const Strided& b) {
     return at >= wa && at + wb <= row;
 }
 
-template <typename T>
-ret_status launch_rotary(const RotArgs& a, bool half, cudaStream_t st) {
-    const size_t total = (size_t)a.B * a.N * (a.x[0].H + a.x[1].H) * (size_t)(a.d - a.rot / 2);
+template <typename T, int VE, bool HALF>
+ret_status launch_rotary_vec(const RotArgs& a, cudaStream_t st) {
+    constexpr int kItems = HALF ? 4 : 8;      // 128 bytes of x in flight per thread either way
+    constexpr int kTableBytes = 32 * 1024;    // most shared memory for cos and sin
+    RotPlan pl;
+    pl.half_units = HALF ? a.rot / 2 / VE : 0;
+    const int units = HALF ? pl.half_units + (a.d - a.rot) / VE : a.d / VE, heads = a.x[0].H + a.x[1].H;
+    pl.units = FastDiv((unsigned)units);
+    pl.heads = FastDiv((unsigned)heads);
+    pl.N = FastDiv((unsigned)a.N);
+    pl.stride = (a.rot / 2 + VE - 1) / VE * VE;  // whole vectors, also past the last frequency
+    // one trip of the block's loop, unless the table or a single token needs more
+    const long long per_token = (long long)units * heads, all = (long long)a.B * a.N;
+    long long tokens = std::max<long long>(1, kRotThreads * kItems / per_token);
+    if (pl.stride) tokens = std::min<long long>(tokens, std::max(1, kTableBytes / (8 * pl.stride)));
+    pl.tokens = (int)std::min(tokens, all);
+    const size_t smem = (size_t)8 * pl.tokens * pl.stride;
+    rotary_vec_kernel<T, VE, HALF, kItems><<<(unsigned)((all + pl.tokens - 1) / pl.tokens), kRotThreads, smem, st>>>(
+        a, pl);
+    return launch_status();
+}
+
+// The widest vectors that every row of every view starts on and that the layout's parts are
+// whole numbers of; elements one by one where that is less than a pair (4 bytes).
+template <typename T, bool HALF>
+ret_status launch_rotary(const RotArgs& a, cudaStream_t st) {
+    constexpr int kE = 16 / (int)sizeof(T);
+    const long long units = a.d, heads = a.x[0].H + a.x[1].H;
+    auto fits = [&](int ve) {
+        const size_t bytes = ve * sizeof(T);
+        if (a.d % ve != 0 || (HALF && a.rot / 2 % ve != 0)) return false;
+        for (const RotView& v : a.x) {
+            if (v.H == 0) continue;
+            for (const void* p : {v.in, static_cast<const void*>(v.out)})
+                if (reinterpret_cast<uintptr_t>(p) % bytes != 0) return false;
+            const long long st3[3][2] = {{v.ib, v.ob}, {v.in_, v.on}, {v.ih, v.oh}};
+            const int n[3] = {a.B, a.N, v.H};
+            for (int i = 0; i < 3; ++i)
+                if (n[i] > 1 && (st3[i][0] % ve != 0 || st3[i][1] % ve != 0)) return false;
+        }
+        return true;
+    };
+    // a token's items and all tokens are counted in 31 bits; the table of one token fits 32 KB
+    const bool small = units * heads < (1LL << 30) && (long long)a.B * a.N < (1LL << 31) && a.rot <= 8192;
+    if (small && fits(kE)) return launch_rotary_vec<T, kE, HALF>(a, st);
+    if (small && fits(kE / 2)) return launch_rotary_vec<T, kE / 2, HALF>(a, st);
+    if (sizeof(T) == 2 && small && fits(2)) return launch_rotary_vec<T, 2, HALF>(a, st);
+    const size_t total = (size_t)a.B * a.N * (size_t)heads * (size_t)(a.d - a.rot / 2);
     const unsigned grid = (unsigned)std::min<size_t>((total + kRotThreads - 1) / kRotThreads, (size_t)32 * tc::sm_count());
-    if (half)
-        rotary_kernel<T, true><<<grid, kRotThreads, 0, st>>>(a, total);
-    else
-        rotary_kernel<T, false><<<grid, kRotThreads, 0, st>>>(a, total);
+    rotary_kernel<T, HALF><<<grid, kRotThreads, 0, st>>>(a, total);
     return launch_status();
 }
 
@@ -1156,8 +1198,10 @@ ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, co
     a.amplitude = amplitude;
     a.sign = inverse ? -1.f : 1.f;
     cudaStream_t st = as_stream(stream);
-    if (dt == RET_BF16) return launch_rotary<__nv_bfloat16>(a, layout == RET_ROTARY_HALF, st);
-    return launch_rotary<float>(a, layout == RET_ROTARY_HALF, st);
+    if (dt == RET_BF16)
+        return layout == RET_ROTARY_HALF ? launch_rotary<__nv_bfloat16, true>(a, st)
+                                         : launch_rotary<__nv_bfloat16, false>(a, st);
+    return layout == RET_ROTARY_HALF ? launch_rotary<float, true>(a, st) : launch_rotary<float, false>(a, st);
 }
 
 ret_status ret_layer_norm(const void* x, const void* residual, const void* weight, const void* bias, void* y,
