@@ -539,25 +539,32 @@ bool disjoint(const Strided& a, const Strided& b) {
     return at >= wa && at + wb <= row;
 }
 
+inline int rotary_units(const RotArgs& a, bool half, int ve) {
+    return half ? a.rot / 2 / ve + (a.d - a.rot) / ve : a.d / ve;
+}
+
 template <typename T, int VE, bool HALF>
 ret_status launch_rotary_vec(const RotArgs& a, cudaStream_t st) {
-    constexpr int kItems = HALF ? 4 : 8;      // 128 bytes of x in flight per thread either way
-    constexpr int kTableBytes = 32 * 1024;    // most shared memory for cos and sin
+    constexpr int kTableBytes = 32 * 1024;  // most shared memory for cos and sin
     RotPlan pl;
     pl.half_units = HALF ? a.rot / 2 / VE : 0;
-    const int units = HALF ? pl.half_units + (a.d - a.rot) / VE : a.d / VE, heads = a.x[0].H + a.x[1].H;
-    pl.units = FastDiv((unsigned)units);
-    pl.heads = FastDiv((unsigned)heads);
-    pl.N = FastDiv((unsigned)a.N);
-    pl.stride = (a.rot / 2 + VE - 1) / VE * VE;  // whole vectors, also past the last frequency
-    // one trip of the block's loop, unless the table or a single token needs more
-    const long long per_token = (long long)units * heads, all = (long long)a.B * a.N;
-    long long tokens = std::max<long long>(1, kRotThreads * kItems / per_token);
+    pl.tensors = a.x[1].H > 0 ? 2 : 1;
+    const int units = rotary_units(a, HALF, VE), heads = std::max(a.x[0].H, a.x[1].H);
+    const int groups = std::max(1, kRotThreads / (units * pl.tensors));  // head groups of a block's q (or k)
+    pl.stride = (a.rot / 2 + VE - 1) / VE * VE;  // whole vectors
+    const long long all = (long long)a.B * a.N;
+    // head groups of a token: one batch of rows per thread, or as many threads as there are heads
+    // where that leaves SMs idle (decode)
+    int split = std::min(groups, (heads + kRotBatch - 1) / kRotBatch);
+    if (all * split < (long long)groups * 2 * tc::sm_count()) split = std::min(groups, heads);
+    long long tokens = groups / split;
     if (pl.stride) tokens = std::min<long long>(tokens, std::max(1, kTableBytes / (8 * pl.stride)));
     pl.tokens = (int)std::min(tokens, all);
+    pl.units = FastDiv((unsigned)units);
+    pl.split = FastDiv((unsigned)split);
+    pl.N = FastDiv((unsigned)a.N);
     const size_t smem = (size_t)8 * pl.tokens * pl.stride;
-    rotary_vec_kernel<T, VE, HALF, kItems><<<(unsigned)((all + pl.tokens - 1) / pl.tokens), kRotThreads, smem, st>>>(
-        a, pl);
+    rotary_vec_kernel<T, VE, HALF><<<(unsigned)((all + pl.tokens - 1) / pl.tokens), kRotThreads, smem, st>>>(a, pl);
     return launch_status();
 }
 
@@ -566,10 +573,11 @@ ret_status launch_rotary_vec(const RotArgs& a, cudaStream_t st) {
 template <typename T, bool HALF>
 ret_status launch_rotary(const RotArgs& a, cudaStream_t st) {
     constexpr int kE = 16 / (int)sizeof(T);
-    const long long units = a.d, heads = a.x[0].H + a.x[1].H;
     auto fits = [&](int ve) {
         const size_t bytes = ve * sizeof(T);
-        if (a.d % ve != 0 || (HALF && a.rot / 2 % ve != 0)) return false;
+        if (a.d % ve != 0 || (HALF && a.rot / 2 % ve != 0) ||
+            rotary_units(a, HALF, ve) * (a.x[1].H > 0 ? 2 : 1) > kRotThreads)
+            return false;
         for (const RotView& v : a.x) {
             if (v.H == 0) continue;
             for (const void* p : {v.in, static_cast<const void*>(v.out)})
@@ -581,12 +589,11 @@ ret_status launch_rotary(const RotArgs& a, cudaStream_t st) {
         }
         return true;
     };
-    // a token's items and all tokens are counted in 31 bits; the table of one token fits 32 KB
-    const bool small = units * heads < (1LL << 30) && (long long)a.B * a.N < (1LL << 31) && a.rot <= 8192;
+    const bool small = (long long)a.B * a.N < (1LL << 31);  // tokens are counted in 31 bits
     if (small && fits(kE)) return launch_rotary_vec<T, kE, HALF>(a, st);
     if (small && fits(kE / 2)) return launch_rotary_vec<T, kE / 2, HALF>(a, st);
     if (sizeof(T) == 2 && small && fits(2)) return launch_rotary_vec<T, 2, HALF>(a, st);
-    const size_t total = (size_t)a.B * a.N * (size_t)heads * (size_t)(a.d - a.rot / 2);
+    const size_t total = (size_t)a.B * a.N * (size_t)(a.x[0].H + a.x[1].H) * (size_t)(a.d - a.rot / 2);
     const unsigned grid = (unsigned)std::min<size_t>((total + kRotThreads - 1) / kRotThreads, (size_t)32 * tc::sm_count());
     rotary_kernel<T, HALF><<<grid, kRotThreads, 0, st>>>(a, total);
     return launch_status();

@@ -50,118 +50,125 @@ __device__ __forceinline__ void rot_angle(const RotArgs& a, long long p, int i, 
     s *= a.amplitude * a.sign;
 }
 
-// Vectors of VE elements: the items (token, head, unit) of a block's `tokens` tokens are spread
-// over its threads, unit fastest, so that a warp reads and writes whole stretches of a head's
-// row. A unit is VE consecutive elements (VE / 2 pairs) in the interleaved layout, and in the
-// half layout the two vectors whose elements pair up, or one vector behind the rotated part.
-// cos and sin of a token are formed once per block, in shared memory, and serve all heads of
-// q and k (16 rows in a 1.3B-shaped layer); a block's first loads are in flight meanwhile.
+// Vectors of VE elements. A thread owns one unit of every `split`-th head of a token's q or k: a unit is VE consecutive elements (VE / 2 pairs) in the interleaved layout, and in
+// the half layout the two vectors whose elements pair up, or one vector behind the rotated part.
+// Threads of neighbouring units and heads lie side by side, so a warp reads whole stretches of a
+// token-major row. A block holds `tokens` tokens of `split` head groups of q and of k each.
+// cos and sin of a token are formed once per block, in shared memory, and serve all heads of q
+// and k; a thread's first kRotBatch rows are in flight meanwhile. Index
+// arithmetic is once per thread: with a division per vector instead the kernel was bound by
+// instruction issue (1.3B-shaped 40.6 us).
+constexpr int kRotBatch = 4;
+
 struct RotPlan {
-    FastDiv units, heads, N;  // units of a head; heads of q and k together; tokens of a batch
-    int tokens;            // of a block
-    int half_units;        // half layout: units of two vectors
-    int stride;            // of a token's cos (or sin) in shared memory, in floats
+    FastDiv units, split, N;  // units of a head; head groups of a token's q (or k); tokens of a batch
+    int tensors;              // 2: q and k, 1: q alone
+    int tokens;               // of a block
+    int half_units;           // half layout: units of two vectors
+    int stride;               // of a token's cos (or sin) in shared memory, in floats
 };
 
-template <typename T, int VE, bool HALF, int ITEMS>
-__global__ void __launch_bounds__(kRotThreads) rotary_vec_kernel(const RotArgs a, const RotPlan pl) {
+template <typename T, int VE, bool HALF>
+struct RotUnit {
     using V = Vec<T, VE>;
-    constexpr int P = HALF ? VE : VE / 2;  // frequencies of a unit
+    static constexpr int P = HALF ? VE : VE / 2;  // frequencies of a unit
+    typename V::Raw lo[kRotBatch], hi[HALF ? kRotBatch : 1];
+
+    // rows h, h + step, ... below H, at x and every `stride` elements
+    __device__ __forceinline__ void load(const T* x, long long stride, int h, int step, int H, bool pair, int half) {
+#pragma unroll
+        for (int i = 0; i < kRotBatch; ++i) {
+            if (h + i * step < H) {
+                lo[i] = V::load_cs(x + i * stride);
+                if (HALF && pair) hi[HALF ? i : 0] = V::load_cs(x + i * stride + half);
+            }
+        }
+    }
+
+    // live: how many of the unit's frequencies are rotated; c and s carry the scale m
+    __device__ __forceinline__ void turn_store(T* y, long long stride, int h, int step, int H, int live, int half,
+                                               const float (&c)[P], const float (&s)[P], float m) {
+#pragma unroll
+        for (int i = 0; i < kRotBatch; ++i) {
+            if (h + i * step >= H) continue;
+            float f[VE];
+            V::unpack(lo[i], f);
+            if (HALF) {
+                if (live > 0) {
+                    float g[VE];
+                    V::unpack(hi[HALF ? i : 0], g);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) {
+                        const float p = f[e], q = g[e];
+                        f[e] = p * c[e % P] - q * s[e % P];
+                        g[e] = p * s[e % P] + q * c[e % P];
+                    }
+                    V::store(y + i * stride + half, g);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) f[e] *= m;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE / 2; ++e) {
+                    const float p = f[2 * e], q = f[2 * e + 1];
+                    const bool on = e < live;
+                    f[2 * e] = on ? p * c[e % P] - q * s[e % P] : p * m;
+                    f[2 * e + 1] = on ? p * s[e % P] + q * c[e % P] : q * m;
+                }
+            }
+            V::store(y + i * stride, f);
+        }
+    }
+};
+
+template <typename T, int VE, bool HALF>
+__global__ void __launch_bounds__(kRotThreads) rotary_vec_kernel(const RotArgs a, const RotPlan pl) {
+    using Unit = RotUnit<T, VE, HALF>;
+    constexpr int P = Unit::P;
     extern __shared__ float4 rot_sm[];
     float* cs = reinterpret_cast<float*>(rot_sm);
     float* sn = cs + pl.tokens * pl.stride;
     const unsigned all = (unsigned)a.B * a.N, first = blockIdx.x * (unsigned)pl.tokens;  // below 2^31
-    const int tokens = (int)min((unsigned)pl.tokens, all - first);
-    const unsigned total = (unsigned)tokens * pl.heads.d * pl.units.d;
-    const int half = a.rot / 2;
-    struct Item {
-        T* y;
-        float scale;
-        int t, u;
-        typename V::Raw lo, hi;
-    };
-    for (unsigned w0 = 0; w0 < total; w0 += kRotThreads * ITEMS) {
-        Item it[ITEMS];
+    const int tokens = (int)min((unsigned)pl.tokens, all - first), half = a.rot / 2;
+    unsigned group, u, t, g, b, n;
+    pl.units.divmod(threadIdx.x, group, u);
+    pl.split.divmod(group, t, g);
+    const bool second = pl.tensors == 2 && (t & 1);
+    if (pl.tensors == 2) t >>= 1;
+    const RotView& v = a.x[second];
+    const bool on = (int)t < tokens;
+    pl.N.divmod(first + t, b, n);
+    const int split = (int)pl.split.d, H = on ? v.H : 0;
+    const bool pair = HALF && (int)u < pl.half_units;
+    const int at = HALF && !pair ? a.rot + ((int)u - pl.half_units) * VE : (int)u * VE;
+    const int live = HALF ? (pair ? P : 0) : min(max(half - (int)u * P, 0), P);
+    const T* x = static_cast<const T*>(v.in) + b * v.ib + n * v.in_ + g * v.ih + at;
+    T* y = static_cast<T*>(v.out) + b * v.ob + n * v.on + g * v.oh + at;
+    const long long si = split * v.ih, so = split * v.oh;
+    Unit r;
+    r.load(x, si, (int)g, split, H, pair, half);
+    for (int j = threadIdx.x; j < tokens * half; j += kRotThreads) {
+        const int tj = j / half, f = j - tj * half;
+        unsigned bj, nj;
+        pl.N.divmod(first + tj, bj, nj);
+        rot_angle(a, rot_position(a, (int)bj, (int)nj), f, cs[tj * pl.stride + f], sn[tj * pl.stride + f]);
+    }
+    __syncthreads();
+    float c[P], s[P];
+    const float m = v.scale;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const unsigned w = w0 + i * kRotThreads + threadIdx.x;
-            if (w >= total) continue;
-            unsigned r, u, t, h, b, n;
-            pl.units.divmod(w, r, u);
-            pl.heads.divmod(r, t, h);
-            const bool second = (int)h >= a.x[0].H;
-            const RotView& v = a.x[second];
-            if (second) h -= a.x[0].H;
-            pl.N.divmod(first + t, b, n);
-            const int at = HALF && (int)u >= pl.half_units ? a.rot + ((int)u - pl.half_units) * VE : (int)u * VE;
-            const T* x = static_cast<const T*>(v.in) + b * v.ib + n * v.in_ + h * v.ih + at;
-            it[i].y = static_cast<T*>(v.out) + b * v.ob + n * v.on + h * v.oh + at;
-            it[i].scale = v.scale;
-            it[i].t = (int)t;
-            it[i].u = (int)u;
-            it[i].lo = V::load_cs(x);
-            if (HALF && (int)u < pl.half_units) it[i].hi = V::load_cs(x + half);
-        }
-        if (w0 == 0) {
-            for (int j = threadIdx.x; j < tokens * half; j += kRotThreads) {
-                const int t = j / half, i = j - t * half;
-                unsigned b, n;
-                pl.N.divmod(first + t, b, n);
-                float c, s;
-                rot_angle(a, rot_position(a, (int)b, (int)n), i, c, s);
-                cs[t * pl.stride + i] = c;
-                sn[t * pl.stride + i] = s;
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < ITEMS; ++i) {
-            const unsigned w = w0 + i * kRotThreads + threadIdx.x;
-            if (w >= total) continue;
-            const float* c = cs + it[i].t * pl.stride + it[i].u * P;
-            const float* s = sn + it[i].t * pl.stride + it[i].u * P;
-            const float m = it[i].scale;
-            float lo[VE];
-            V::unpack(it[i].lo, lo);
-            if (HALF) {
-                if (it[i].u < pl.half_units) {
-                    float hi[VE];
-                    V::unpack(it[i].hi, hi);
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const float p = lo[e], q = hi[e];
-                        lo[e] = m * (p * c[e] - q * s[e]);
-                        hi[e] = m * (p * s[e] + q * c[e]);
-                    }
-                    V::store(it[i].y + half, hi);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) lo[e] *= m;
-                }
-            } else {
-                const int live = min(P, half - it[i].u * P);  // pairs of this unit that are rotated
-                auto turn = [&](int e) {
-                    const float p = lo[2 * e], q = lo[2 * e + 1];
-                    lo[2 * e] = m * (p * c[e] - q * s[e]);
-                    lo[2 * e + 1] = m * (p * s[e] + q * c[e]);
-                };
-                if (live == P) {
-#pragma unroll
-                    for (int e = 0; e < P; ++e) turn(e);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < P; ++e) {
-                        if (e < live) {
-                            turn(e);
-                        } else {
-                            lo[2 * e] *= m;
-                            lo[2 * e + 1] *= m;
-                        }
-                    }
-                }
-            }
-            V::store(it[i].y, lo);
-        }
+    for (int e = 0; e < P; ++e) {
+        c[e] = on && e < live ? m * cs[t * pl.stride + u * P + e] : 0.f;
+        s[e] = on && e < live ? m * sn[t * pl.stride + u * P + e] : 0.f;
+    }
+    for (int h = (int)g;;) {
+        r.turn_store(y, so, h, split, H, live, half, c, s, m);
+        h += kRotBatch * split;
+        if (h >= H) break;
+        x += kRotBatch * si;
+        y += kRotBatch * so;
+        r.load(x, si, h, split, H, pair, half);
     }
 }
 
