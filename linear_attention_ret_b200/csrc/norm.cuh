@@ -170,6 +170,82 @@ __device__ __forceinline__ float sigmoid(float x) {
     return r;
 }
 
+// LPR lanes per row, each with CH vectors of VE elements of dy, o and gate in registers, so a
+// row is read once and all of its loads are in flight before the two sums are reduced.
+// swish(gate) is formed again for the outputs: two more special-function instructions per element
+// cost less than the registers. VE = 1 serves rows that are not whole 16-byte chunks: neighbouring
+// lanes still read neighbouring elements. A row's place takes two 32-bit divisions by
+// multiplication: rows are fewer than 2^31. dgate may be gate or dy, and dout o: an element is
+// read by the thread that writes it.
+template <typename T, int VE, int LPR, int CH>
+__global__ void __launch_bounds__(kNormThreads)
+norm_gate_backward_vec_kernel(const T* dy, const T* o, const T* gate, T* dout, T* dgate, FastDiv H, FastDiv N, int dv,
+                              float eps, unsigned rows) {
+    using V = Vec<T, VE>;
+    constexpr unsigned kRowsPerWarp = 32 / LPR;
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const int chunks = dv / VE;
+    const float inv_dv = 1.f / (float)dv;
+    const unsigned warps = gridDim.x * (kNormThreads / 32);
+    for (unsigned w = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); w * kRowsPerWarp < rows; w += warps) {
+        const unsigned r = w * kRowsPerWarp + lane / LPR;
+        const bool live = r < rows;
+        unsigned bn, h, b, n;
+        H.divmod(live ? r : 0, bn, h);
+        N.divmod(bn, b, n);
+        const size_t o_row = ((size_t)(b * H.d + h) * N.d + n) * dv, y_row = (size_t)(live ? r : 0) * dv;
+        typename V::Raw ov[CH], gv[CH], yv[CH];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int idx = sub + c * LPR;
+            ov[c] = gv[c] = yv[c] = V::zero();
+            if (live && idx < chunks) {
+                ov[c] = V::load_cs(o + o_row + idx * VE);
+                gv[c] = V::load_cs(gate + y_row + idx * VE);
+                yv[c] = V::load_cs(dy + y_row + idx * VE);
+            }
+        }
+        float ss = 0.f, uo = 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            float x[VE], g[VE], d[VE];
+            V::unpack(ov[c], x);
+            V::unpack(gv[c], g);
+            V::unpack(yv[c], d);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                ss = fmaf(x[e], x[e], ss);
+                uo = fmaf(d[e] * (g[e] * sigmoid(g[e])), x[e], uo);
+            }
+        }
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, off);
+            uo += __shfl_xor_sync(0xffffffffu, uo, off);
+        }
+        const float inv_rms = rsqrtf(ss * inv_dv + eps);
+        const float k = inv_rms * inv_rms * (uo * inv_dv);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int idx = sub + c * LPR;
+            if (live && idx < chunks) {
+                float x[VE], g[VE], d[VE];
+                V::unpack(ov[c], x);
+                V::unpack(gv[c], g);
+                V::unpack(yv[c], d);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float sig = sigmoid(g[e]), sw = g[e] * sig, z = x[e], t = d[e];
+                    x[e] = inv_rms * (t * sw - z * k);
+                    d[e] = t * (z * inv_rms) * (sig + sw * (1.f - sig));
+                }
+                V::store(dout + o_row + idx * VE, x);
+                V::store(dgate + y_row + idx * VE, d);
+            }
+        }
+    }
+}
+
 // Any dv and alignment: one warp per row, two passes over the row (the second from L1/L2).
 // dgate may be gate or dy, and dout o: an element is read by the thread that writes it.
 template <typename T>

@@ -540,7 +540,7 @@ bool disjoint(const Strided& a, const Strided& b) {
 }
 
 inline int rotary_units(const RotArgs& a, bool half, int ve) {
-    return half ? a.rot / 2 / ve + (a.d - a.rot) / ve : a.d / ve;
+    return half ? a.rot / 2 / ve + ((a.d - a.rot) / ve + 1) / 2 : a.d / ve;
 }
 
 template <typename T, int VE, bool HALF>
@@ -646,15 +646,51 @@ ret_status launch_layer_norm_backward(const void* dy, const void* x, const void*
     return launch_status();
 }
 
+template <typename T, int VE, int LPR, int CH>
+ret_status launch_norm_backward_vec(const T* dy, const T* o, const T* gate, T* dout, T* dgate, int H, int N, int dv,
+                                    float eps, size_t rows, cudaStream_t st) {
+    const size_t rows_per_block = (size_t)(kNormThreads / 32) * (32 / LPR);
+    const size_t blocks = std::min<size_t>((rows + rows_per_block - 1) / rows_per_block, (size_t)32 * tc::sm_count());
+    norm_gate_backward_vec_kernel<T, VE, LPR, CH><<<(unsigned)blocks, kNormThreads, 0, st>>>(
+        dy, o, gate, dout, dgate, FastDiv((unsigned)H), FastDiv((unsigned)N), dv, eps, (unsigned)rows);
+    return launch_status();
+}
+
+// Rows in registers: whole 16-byte chunks on up to 32 lanes, or single elements on 32 lanes where
+// rows are not whole chunks; longer rows (and 2^30 rows and more) in two passes.
 template <typename T>
-ret_status launch_norm_gate_backward(const void* dy, const void* o, const void* gate, void* dout, void* dgate, int B,
-                                     int H, int N, int dv, float eps, cudaStream_t st) {
+ret_status launch_norm_gate_backward(const void* dy_, const void* o_, const void* gate_, void* dout_, void* dgate_,
+                                     int B, int H, int N, int dv, float eps, cudaStream_t st) {
+    constexpr int kE = 16 / (int)sizeof(T);
+    const T *dy = static_cast<const T*>(dy_), *o = static_cast<const T*>(o_), *gate = static_cast<const T*>(gate_);
+    T *dout = static_cast<T*>(dout_), *dgate = static_cast<T*>(dgate_);
     const size_t rows = (size_t)B * N * H;
+    const bool vec = dv % kE == 0 && aligned16(dy) && aligned16(o) && aligned16(gate) && aligned16(dout) &&
+                     aligned16(dgate);
+#define RET_NORM_BACKWARD(VE, LPR, CH) \
+    if (dv <= VE * LPR * CH) return launch_norm_backward_vec<T, VE, LPR, CH>(dy, o, gate, dout, dgate, H, N, dv, eps, rows, st)
+    if (rows < (1u << 30) && vec) {
+        RET_NORM_BACKWARD(kE, 1, 1);
+        RET_NORM_BACKWARD(kE, 2, 1);
+        RET_NORM_BACKWARD(kE, 4, 1);
+        RET_NORM_BACKWARD(kE, 8, 1);
+        RET_NORM_BACKWARD(kE, 16, 1);
+        RET_NORM_BACKWARD(kE, 32, 1);
+        RET_NORM_BACKWARD(kE, 32, 2);
+        RET_NORM_BACKWARD(kE, 32, 4);
+        RET_NORM_BACKWARD(kE, 32, 8);
+    } else if (rows < (1u << 30)) {
+        RET_NORM_BACKWARD(1, 32, 2);
+        RET_NORM_BACKWARD(1, 32, 4);
+        RET_NORM_BACKWARD(1, 32, 8);
+        RET_NORM_BACKWARD(1, 32, 16);
+        RET_NORM_BACKWARD(1, 32, 32);
+    }
+#undef RET_NORM_BACKWARD
     const size_t blocks = std::min<size_t>((rows + kNormThreads / 32 - 1) / (kNormThreads / 32),
                                            (size_t)32 * tc::sm_count());
-    norm_gate_backward_scalar_kernel<T><<<(unsigned)blocks, kNormThreads, 0, st>>>(
-        static_cast<const T*>(dy), static_cast<const T*>(o), static_cast<const T*>(gate), static_cast<T*>(dout),
-        static_cast<T*>(dgate), H, N, dv, eps, rows);
+    norm_gate_backward_scalar_kernel<T><<<(unsigned)blocks, kNormThreads, 0, st>>>(dy, o, gate, dout, dgate, H, N, dv,
+                                                                                  eps, rows);
     return launch_status();
 }
 

@@ -51,20 +51,20 @@ __device__ __forceinline__ void rot_angle(const RotArgs& a, long long p, int i, 
 }
 
 // Vectors of VE elements. A thread owns one unit of every `split`-th head of a token's q or k: a unit is VE consecutive elements (VE / 2 pairs) in the interleaved layout, and in
-// the half layout the two vectors whose elements pair up, or one vector behind the rotated part.
-// Threads of neighbouring units and heads lie side by side, so a warp reads whole stretches of a
+// the half layout two vectors: those whose elements pair up, or two neighbours behind the rotated
+// part. Threads of neighbouring units and heads lie side by side, so a warp reads whole stretches of a
 // token-major row. A block holds `tokens` tokens of `split` head groups of q and of k each.
 // cos and sin of a token are formed once per block, in shared memory, and serve all heads of q
 // and k; a thread's first kRotBatch rows are in flight meanwhile. Index
-// arithmetic is once per thread: with a division per vector instead the kernel was bound by
-// instruction issue (1.3B-shaped 40.6 us).
+// arithmetic is once per thread: with divisions per vector the kernel was bound by instruction
+// issue (1.3B-shaped, 134 MB: 40.6 us, now 23.1 us, 5.8 TB/s; batches of two rows 25.9 us).
 constexpr int kRotBatch = 4;
 
 struct RotPlan {
     FastDiv units, split, N;  // units of a head; head groups of a token's q (or k); tokens of a batch
     int tensors;              // 2: q and k, 1: q alone
     int tokens;               // of a block
-    int half_units;           // half layout: units of two vectors
+    int half_units;           // half layout: units that are rotated
     int stride;               // of a token's cos (or sin) in shared memory, in floats
 };
 
@@ -74,19 +74,21 @@ struct RotUnit {
     static constexpr int P = HALF ? VE : VE / 2;  // frequencies of a unit
     typename V::Raw lo[kRotBatch], hi[HALF ? kRotBatch : 1];
 
-    // rows h, h + step, ... below H, at x and every `stride` elements
-    __device__ __forceinline__ void load(const T* x, long long stride, int h, int step, int H, bool pair, int half) {
+    // rows h, h + step, ... below H, at x and every `stride` elements; the second vector `second`
+    // elements on (half layout, 0: there is none)
+    __device__ __forceinline__ void load(const T* x, long long stride, int h, int step, int H, int second) {
 #pragma unroll
         for (int i = 0; i < kRotBatch; ++i) {
             if (h + i * step < H) {
                 lo[i] = V::load_cs(x + i * stride);
-                if (HALF && pair) hi[HALF ? i : 0] = V::load_cs(x + i * stride + half);
+                if (HALF && second) hi[HALF ? i : 0] = V::load_cs(x + i * stride + second);
             }
         }
     }
 
-    // live: how many of the unit's frequencies are rotated; c and s carry the scale m
-    __device__ __forceinline__ void turn_store(T* y, long long stride, int h, int step, int H, int live, int half,
+    // live: how many of the unit's frequencies are rotated; c and s carry the scale m. Elements
+    // that are not rotated are selected, not multiplied by 0: a neighbour may be infinite.
+    __device__ __forceinline__ void turn_store(T* y, long long stride, int h, int step, int H, int second, int live,
                                                const float (&c)[P], const float (&s)[P], float m) {
 #pragma unroll
         for (int i = 0; i < kRotBatch; ++i) {
@@ -94,27 +96,21 @@ struct RotUnit {
             float f[VE];
             V::unpack(lo[i], f);
             if (HALF) {
-                if (live > 0) {
-                    float g[VE];
-                    V::unpack(hi[HALF ? i : 0], g);
+                float g[VE];
+                V::unpack(hi[HALF ? i : 0], g);
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const float p = f[e], q = g[e];
-                        f[e] = p * c[e % P] - q * s[e % P];
-                        g[e] = p * s[e % P] + q * c[e % P];
-                    }
-                    V::store(y + i * stride + half, g);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) f[e] *= m;
+                for (int e = 0; e < VE; ++e) {
+                    const float p = f[e], q = g[e];
+                    f[e] = live ? p * c[e % P] - q * s[e % P] : p * m;
+                    g[e] = live ? p * s[e % P] + q * c[e % P] : q * m;
                 }
+                if (second) V::store(y + i * stride + second, g);
             } else {
 #pragma unroll
                 for (int e = 0; e < VE / 2; ++e) {
                     const float p = f[2 * e], q = f[2 * e + 1];
-                    const bool on = e < live;
-                    f[2 * e] = on ? p * c[e % P] - q * s[e % P] : p * m;
-                    f[2 * e + 1] = on ? p * s[e % P] + q * c[e % P] : q * m;
+                    f[2 * e] = e < live ? p * c[e % P] - q * s[e % P] : p * m;
+                    f[2 * e + 1] = e < live ? p * s[e % P] + q * c[e % P] : q * m;
                 }
             }
             V::store(y + i * stride, f);
@@ -122,8 +118,10 @@ struct RotUnit {
     }
 };
 
+// Three blocks per SM: the half layout's two vectors per row otherwise take 98 registers and two
+// blocks (gradient at the gated layer's shapes 54.0 us against 50.3 us).
 template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kRotThreads) rotary_vec_kernel(const RotArgs a, const RotPlan pl) {
+__global__ void __launch_bounds__(kRotThreads, 3) rotary_vec_kernel(const RotArgs a, const RotPlan pl) {
     using Unit = RotUnit<T, VE, HALF>;
     constexpr int P = Unit::P;
     extern __shared__ float4 rot_sm[];
@@ -141,13 +139,14 @@ __global__ void __launch_bounds__(kRotThreads) rotary_vec_kernel(const RotArgs a
     pl.N.divmod(first + t, b, n);
     const int split = (int)pl.split.d, H = on ? v.H : 0;
     const bool pair = HALF && (int)u < pl.half_units;
-    const int at = HALF && !pair ? a.rot + ((int)u - pl.half_units) * VE : (int)u * VE;
+    const int at = HALF && !pair ? a.rot + ((int)u - pl.half_units) * 2 * VE : (int)u * VE;
+    const int second_at = !HALF ? 0 : pair ? half : at + VE < a.d ? VE : 0;
     const int live = HALF ? (pair ? P : 0) : min(max(half - (int)u * P, 0), P);
     const T* x = static_cast<const T*>(v.in) + b * v.ib + n * v.in_ + g * v.ih + at;
     T* y = static_cast<T*>(v.out) + b * v.ob + n * v.on + g * v.oh + at;
     const long long si = split * v.ih, so = split * v.oh;
     Unit r;
-    r.load(x, si, (int)g, split, H, pair, half);
+    r.load(x, si, (int)g, split, H, second_at);
     for (int j = threadIdx.x; j < tokens * half; j += kRotThreads) {
         const int tj = j / half, f = j - tj * half;
         unsigned bj, nj;
@@ -163,12 +162,12 @@ __global__ void __launch_bounds__(kRotThreads) rotary_vec_kernel(const RotArgs a
         s[e] = on && e < live ? m * sn[t * pl.stride + u * P + e] : 0.f;
     }
     for (int h = (int)g;;) {
-        r.turn_store(y, so, h, split, H, live, half, c, s, m);
+        r.turn_store(y, so, h, split, H, second_at, live, c, s, m);
         h += kRotBatch * split;
         if (h >= H) break;
         x += kRotBatch * si;
         y += kRotBatch * so;
-        r.load(x, si, h, split, H, pair, half);
+        r.load(x, si, h, split, H, second_at);
     }
 }
 
