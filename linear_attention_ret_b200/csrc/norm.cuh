@@ -177,8 +177,12 @@ __device__ __forceinline__ float sigmoid(float x) {
 // lanes still read neighbouring elements. A row's place takes two 32-bit divisions by
 // multiplication: rows are fewer than 2^31. dgate may be gate or dy, and dout o: an element is
 // read by the thread that writes it.
+//
+// Blocks per SM: left alone, the two-vector form (dv = 512) keeps the first pass's unpacked
+// values, 93 registers and two blocks: 60.2 us at the 1.3B-shaped output (336 MB), 55.3 us with three
+// blocks (6.07 TB/s), 59.8 us with four, which spill.
 template <typename T, int VE, int LPR, int CH>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, VE * CH * sizeof(T) <= 32 ? 3 : VE * CH * sizeof(T) <= 64 ? 2 : 1)
 norm_gate_backward_vec_kernel(const T* dy, const T* o, const T* gate, T* dout, T* dgate, FastDiv H, FastDiv N, int dv,
                               float eps, unsigned rows) {
     using V = Vec<T, VE>;

@@ -605,21 +605,120 @@ inline unsigned block_rows(long long rows) {
     return (unsigned)std::min<long long>(rows, (long long)32 * tc::sm_count());
 }
 
-template <typename T, typename W>
-ret_status launch_layer_norm(const void* x, const void* res, const void* w, const void* b, void* y, void* sum_out,
-                             float* mean, float* rstd, long long rows, int D, float eps, cudaStream_t st) {
-    ln_forward_rows_kernel<T, W><<<block_rows(rows), kLnThreads, 0, st>>>(
-        static_cast<const T*>(x), static_cast<const T*>(res), static_cast<const W*>(w), static_cast<const W*>(b),
-        static_cast<T*>(y), static_cast<T*>(sum_out), mean, rstd, (size_t)rows, D, eps);
+inline int lanes_for(int chunks) {  // a power of two up to 32
+    int n = 1;
+    while (n < chunks && n < 32) n *= 2;
+    return n;
+}
+inline int warp_threads(int n) { return (n + 31) / 32 * 32; }
+
+template <typename T, typename W, int VE, int EPT, bool WARP>
+ret_status launch_ln_forward(const T* x, const T* res, const W* w, const W* b, T* y, T* sum_out, float* mean,
+                             float* rstd, long long rows, int D, float eps, cudaStream_t st) {
+    const int chunks = D / VE;
+    const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
+    const long long per_block = WARP ? kLnThreads / lanes : 1;
+    ln_forward_kernel<T, W, VE, EPT, WARP><<<(unsigned)((rows + per_block - 1) / per_block), WARP ? kLnThreads : lanes,
+                                             0, st>>>(x, res, w, b, y, sum_out, mean, rstd, (unsigned)rows, D, eps,
+                                                      lanes);
     return launch_status();
 }
 
+template <typename T, typename W, int VE>
+ret_status launch_ln_forward_width(const T* x, const T* res, const W* w, const W* b, T* y, T* sum_out, float* mean,
+                                   float* rstd, long long rows, int D, float eps, cudaStream_t st) {
+    if (D <= 32 * 8) return launch_ln_forward<T, W, VE, 8, true>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+    if (D <= 32 * 16) return launch_ln_forward<T, W, VE, 16, true>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+    if (D <= 32 * 32) return launch_ln_forward<T, W, VE, 32, true>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+    if (D <= 256 * 8) return launch_ln_forward<T, W, VE, 8, false>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+    if (D <= 512 * 16) return launch_ln_forward<T, W, VE, 16, false>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+    return launch_ln_forward<T, W, VE, 32, false>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+}
+
+// Rows in registers up to 32,768 elements, in 16-byte vectors where every row starts on 16 bytes,
+// else element by element; longer rows (and 2^31 rows and more) in three passes.
 template <typename T, typename W>
-ret_status launch_layer_norm_backward(const void* dy, const void* x, const void* w, const float* mean,
-                                      const float* rstd, const void* dsum, void* dx, void* dw, void* db,
+ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, const void* b_, void* y_,
+                             void* sum_out_, float* mean, float* rstd, long long rows, int D, float eps,
+                             cudaStream_t st) {
+    constexpr int kE = 16 / (int)sizeof(T);
+    const T *x = static_cast<const T*>(x_), *res = static_cast<const T*>(res_);
+    const W *w = static_cast<const W*>(w_), *b = static_cast<const W*>(b_);
+    T *y = static_cast<T*>(y_), *sum_out = static_cast<T*>(sum_out_);
+    if (D <= 32 * 1024 && rows < (1LL << 31)) {
+        if (D % kE == 0 && aligned16(x) && aligned16(res) && aligned16(w) && aligned16(b) && aligned16(y) &&
+            aligned16(sum_out))
+            return launch_ln_forward_width<T, W, kE>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+        return launch_ln_forward_width<T, W, 1>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+    }
+    ln_forward_rows_kernel<T, W><<<block_rows(rows), kLnThreads, 0, st>>>(x, res, w, b, y, sum_out, mean, rstd,
+                                                                          (size_t)rows, D, eps);
+    return launch_status();
+}
+
+template <typename T, typename W, int VE, int EPT, bool WARP>
+int ln_backward_grid(long long rows, int lanes, int threads, size_t smem) {
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ln_backward_kernel<T, W, VE, EPT, WARP>, threads,
+                                                      smem) != cudaSuccess || per_sm < 1)
+        per_sm = 1;
+    const long long per_block = WARP ? threads / lanes : 1;
+    return (int)std::min<long long>((rows + per_block - 1) / per_block, (long long)per_sm * tc::sm_count());
+}
+
+// One pass over dy and x. Returns the number of partial rows that it leaves in *part (allocated here).
+template <typename T, typename W, int VE, int EPT, bool WARP>
+ret_status launch_ln_backward(const T* dy, const T* x, const W* w, const float* mean, const float* rstd, const T* dsum,
+                              T* dx, W* dw, W* db, long long rows, int D, cudaStream_t st) {
+    const int chunks = D / VE;
+    const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
+    const int threads = WARP ? kLnThreads : lanes;
+    const size_t smem = WARP ? sizeof(float) * 2 * D : 0;
+    const int grid = ln_backward_grid<T, W, VE, EPT, WARP>(rows, lanes, threads, smem);
+    float* part = nullptr;
+    if (dw || db) {
+        tc::keep_pool_memory();
+        if (cudaMallocAsync(reinterpret_cast<void**>(&part), sizeof(float) * 2 * (size_t)grid * D, st) != cudaSuccess)
+            return RET_ERR_CUDA;
+    }
+    ln_backward_kernel<T, W, VE, EPT, WARP><<<grid, threads, smem, st>>>(dy, x, w, mean, rstd, dsum, dx, part,
+                                                                        (unsigned)rows, D, lanes);
+    ret_status r = launch_status();
+    if (part) {
+        if (r == RET_OK) {
+            ln_reduce_kernel<W><<<(unsigned)((2LL * D + 31) / 32), kLnThreads, 0, st>>>(part, grid, dw, db, D);
+            r = launch_status();
+        }
+        if (cudaFreeAsync(part, st) != cudaSuccess && r == RET_OK) r = RET_ERR_CUDA;
+    }
+    return r;
+}
+
+template <typename T, typename W, int VE>
+ret_status launch_ln_backward_width(const T* dy, const T* x, const W* w, const float* mean, const float* rstd,
+                                    const T* dsum, T* dx, W* dw, W* db, long long rows, int D, cudaStream_t st) {
+    if (D <= 32 * 8) return launch_ln_backward<T, W, VE, 8, true>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
+    if (D <= 32 * 16) return launch_ln_backward<T, W, VE, 16, true>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
+    if (D <= 512 * 8) return launch_ln_backward<T, W, VE, 8, false>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
+    return launch_ln_backward<T, W, VE, 16, false>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
+}
+
+// Up to 8,192 columns in one pass; wider (and 2^30 rows and more): the column sums and dx in a
+// pass of their own each.
+template <typename T, typename W>
+ret_status launch_layer_norm_backward(const void* dy_, const void* x_, const void* w_, const float* mean,
+                                      const float* rstd, const void* dsum_, void* dx_, void* dw_, void* db_,
                                       long long rows, int D, cudaStream_t st) {
-    const T* dyp = static_cast<const T*>(dy);
-    const T* xp = static_cast<const T*>(x);
+    constexpr int kE = 16 / (int)sizeof(T);
+    const T *dy = static_cast<const T*>(dy_), *x = static_cast<const T*>(x_), *dsum = static_cast<const T*>(dsum_);
+    const W* w = static_cast<const W*>(w_);
+    T* dx = static_cast<T*>(dx_);
+    W *dw = static_cast<W*>(dw_), *db = static_cast<W*>(db_);
+    if (D <= 8192 && rows < (1LL << 30)) {
+        if (D % kE == 0 && aligned16(dy) && aligned16(x) && aligned16(w) && aligned16(dsum) && aligned16(dx))
+            return launch_ln_backward_width<T, W, kE>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
+        return launch_ln_backward_width<T, W, 1>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
+    }
     ret_status r = RET_OK;
     if (dw || db) {
         const unsigned cols = (unsigned)((D + kLnThreads - 1) / kLnThreads);
@@ -628,21 +727,19 @@ ret_status launch_layer_norm_backward(const void* dy, const void* x, const void*
         float* part = nullptr;
         if (cudaMallocAsync(reinterpret_cast<void**>(&part), sizeof(float) * 2 * (size_t)parts * D, st) != cudaSuccess)
             return RET_ERR_CUDA;
-        ln_backward_columns_kernel<T><<<dim3(cols, parts), kLnThreads, 0, st>>>(dyp, xp, mean, rstd, part, (size_t)rows,
+        ln_backward_columns_kernel<T><<<dim3(cols, parts), kLnThreads, 0, st>>>(dy, x, mean, rstd, part, (size_t)rows,
                                                                                D);
         r = launch_status();
         if (r == RET_OK) {
-            ln_reduce_kernel<W><<<cols, kLnThreads, 0, st>>>(part, (int)parts, static_cast<W*>(dw),
-                                                             static_cast<W*>(db), D);
+            ln_reduce_kernel<W><<<(unsigned)((2LL * D + 31) / 32), kLnThreads, 0, st>>>(part, (int)parts, dw, db, D);
             r = launch_status();
         }
         if (cudaFreeAsync(part, st) != cudaSuccess && r == RET_OK) r = RET_ERR_CUDA;
         if (r != RET_OK) return r;
     }
     // last: dx may take dy's place
-    ln_backward_rows_kernel<T, W><<<block_rows(rows), kLnThreads, 0, st>>>(
-        dyp, xp, static_cast<const W*>(w), mean, rstd, static_cast<const T*>(dsum), static_cast<T*>(dx), (size_t)rows,
-        D);
+    ln_backward_rows_kernel<T, W><<<block_rows(rows), kLnThreads, 0, st>>>(dy, x, w, mean, rstd, dsum, dx, (size_t)rows,
+                                                                           D);
     return launch_status();
 }
 
