@@ -71,6 +71,39 @@ struct Vec {
     }
 };
 
+// Two floats that one instruction adds, multiplies or fuses (fma.rn.f32x2 and its kin, sm_100):
+// each half is rounded as the scalar operation rounds it.
+struct F2 {
+    unsigned long long v;
+    F2() = default;
+    __device__ __forceinline__ F2(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+    __device__ __forceinline__ float lo() const { return halves(true); }
+    __device__ __forceinline__ float hi() const { return halves(false); }
+    __device__ __forceinline__ float sum() const { return lo() + hi(); }
+
+  private:
+    __device__ __forceinline__ float halves(bool low) const {
+        float a, b;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+        return low ? a : b;
+    }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
 // Division of a 32-bit number by a fixed 32-bit d >= 1, exact for every n < 2^31: with
 // l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1, n / d = (umulhi(m, n) + n) >> l
 // (Granlund and Montgomery, Division by invariant integers using multiplication, 1994).

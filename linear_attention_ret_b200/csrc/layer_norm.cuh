@@ -57,83 +57,141 @@ __device__ __forceinline__ void row_sums(float (&v)[K], int lanes, float (*sm)[3
     }
 }
 
-// One row per `lanes` lanes of a warp (WARP), or per block; a thread keeps EPT elements of it, in
-// vectors of VE, as floats: the row is read once, and the mean and then the centred squares are
-// summed from registers.
-template <typename T, typename W, int VE, int EPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? kLnThreads : 1024)
-ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const W* __restrict__ bias, T* y, T* sum_out,
-                  float* __restrict__ mean, float* __restrict__ rstd, unsigned rows, int D, float eps, int lanes) {
+// A thread's EPT elements of a row: vectors sub, sub + lanes, ... of VE elements, as they are in
+// memory, and as pairs of floats.
+template <typename T, int VE, int EPT>
+struct RowPart {
     using V = Vec<T, VE>;
-    constexpr int CH = EPT / VE;
-    __shared__ __align__(16) float sm[2][1][32];
-    const int sub = WARP ? threadIdx.x & (lanes - 1) : threadIdx.x;
-    const unsigned r = WARP ? (unsigned)((blockIdx.x * (size_t)kLnThreads + threadIdx.x) / lanes) : blockIdx.x;
-    const bool live = r < rows;
-    const size_t at = (size_t)r * D;
-    const int chunks = D / VE;
-    float v[CH][VE];
-    {
-        typename V::Raw xr[CH], rr[CH];
+    static constexpr int CH = EPT / VE;
+    typename V::Raw q[CH];
+
+    __device__ __forceinline__ void load(const T* row, int sub, int lanes, int chunks, bool live) {
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int i = sub + c * lanes;
-            xr[c] = rr[c] = V::zero();
-            if (live && i < chunks) {
-                xr[c] = V::load_cs(x + at + i * VE);
-                if (res) rr[c] = V::load_cs(res + at + i * VE);
-            }
+            q[c] = V::zero();
+            if (live && i < chunks) q[c] = V::load_cs(row + i * VE);
+        }
+    }
+    __device__ __forceinline__ void pairs(F2 (&f)[EPT / 2]) const {
+        float e[EPT];
+#pragma unroll
+        for (int c = 0; c < CH; ++c) V::unpack(q[c], e + c * VE);
+#pragma unroll
+        for (int i = 0; i < EPT / 2; ++i) f[i] = F2(e[2 * i], e[2 * i + 1]);
+    }
+    static __device__ __forceinline__ void store(T* row, const F2 (&f)[EPT / 2], int sub, int lanes, int chunks) {
+        float e[EPT];
+#pragma unroll
+        for (int i = 0; i < EPT / 2; ++i) {
+            e[2 * i] = f[i].lo();
+            e[2 * i + 1] = f[i].hi();
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            V::unpack(xr[c], v[c]);
-            if (res) {
-                float f[VE];
-                V::unpack(rr[c], f);
+            const int i = sub + c * lanes;
+            if (i < chunks) V::store(row + i * VE, e + c * VE);
+        }
+    }
+};
+
+// Pairs of a thread's columns of a weight, `none` where there is no weight or no column.
+template <typename W, int VE, int EPT>
+__device__ __forceinline__ void column_weights(const W* w, float none, F2 (&f)[EPT / 2], int sub, int lanes,
+                                               int chunks) {
+    float e[EPT];
 #pragma unroll
-                for (int e = 0; e < VE; ++e) v[c][e] += f[e];
+    for (int c = 0; c < EPT / VE; ++c) {
+        const int i = sub + c * lanes;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) e[c * VE + k] = none;
+        if (w && i < chunks) ln_weights<W, VE>(w + i * VE, e + c * VE);
+    }
+#pragma unroll
+    for (int i = 0; i < EPT / 2; ++i) f[i] = F2(e[2 * i], e[2 * i + 1]);
+}
+
+// One row per `lanes` lanes of a warp (WARP), or per block; a thread keeps EPT elements of it: the
+// row is read once, and the mean and then the centred squares are summed from registers. Blocks
+// stay and take every gridDim.x-th row; the next row's loads are issued before the current
+// row's sums are reduced. HOLD: the thread's columns of weight and bias stay in registers too, else they
+// are read from L1 for every row.
+template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD>
+__global__ void __launch_bounds__(WARP ? kLnThreads : 512)
+ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const W* __restrict__ bias, T* y, T* sum_out,
+                  float* __restrict__ mean, float* __restrict__ rstd, unsigned rows, int D, float eps, int lanes) {
+    using Part = RowPart<T, VE, EPT>;
+    __shared__ __align__(16) float sm[2][2][1][32];
+    const int sub = WARP ? threadIdx.x & (lanes - 1) : threadIdx.x;
+    const unsigned per_block = WARP ? kLnThreads / lanes : 1, mine = WARP ? threadIdx.x / lanes : 0;
+    const unsigned step = gridDim.x * per_block;
+    const int chunks = D / VE;
+    const float inv = 1.f / (float)D;
+    F2 w[EPT / 2], b[EPT / 2];
+    if (HOLD) {
+        column_weights<W, VE, EPT>(weight, 1.f, w, sub, lanes, chunks);
+        column_weights<W, VE, EPT>(bias, 0.f, b, sub, lanes, chunks);
+    }
+    Part cur, cur_res;
+    unsigned base = blockIdx.x * per_block;  // every thread of a block makes the same trips
+    auto load = [&](Part& p, Part& pr, unsigned r) {
+        p.load(x + (size_t)r * D, sub, lanes, chunks, r < rows);
+        if (res) pr.load(res + (size_t)r * D, sub, lanes, chunks, r < rows);
+    };
+    load(cur, cur_res, base + mine);
+    for (int flip = 0; base < rows; base += step, flip ^= 1) {
+        const unsigned r = base + mine;
+        F2 v[EPT / 2];
+        cur.pairs(v);
+        if (res) {
+            F2 f[EPT / 2];
+            cur_res.pairs(f);
+#pragma unroll
+            for (int i = 0; i < EPT / 2; ++i) v[i] = add2(v[i], f[i]);
+        }
+        load(cur, cur_res, r + step);
+        F2 t = v[0];
+#pragma unroll
+        for (int i = 1; i < EPT / 2; ++i) t = add2(t, v[i]);
+        float s[1] = {t.sum()};
+        row_sums<WARP>(s, lanes, sm[flip][0]);
+        const float mu = s[0] * inv;
+        const F2 minus = F2(-mu, -mu);
+        t = F2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < Part::CH; ++c) {
+            if (sub + c * lanes < chunks) {
+                if (VE == 1) {
+                    const float z = (c & 1 ? v[c / 2].hi() : v[c / 2].lo()) - mu;
+                    t = add2(t, F2(z * z, 0.f));
+                } else {
+#pragma unroll
+                    for (int i = c * VE / 2; i < (c + 1) * VE / 2; ++i) {
+                        const F2 z = add2(v[i], minus);
+                        t = fma2(z, z, t);
+                    }
+                }
             }
         }
-    }
-    const float inv = 1.f / (float)D;
-    float s[1] = {0.f};
+        s[0] = t.sum();
+        row_sums<WARP>(s, lanes, sm[flip][1]);
+        const float rs = rsqrtf(s[0] * inv + eps);
+        if (r < rows) {
+            const size_t at = (size_t)r * D;
+            if (sum_out) Part::store(sum_out + at, v, sub, lanes, chunks);
+            if (!HOLD) {
+                column_weights<W, VE, EPT>(weight, 1.f, w, sub, lanes, chunks);
+                column_weights<W, VE, EPT>(bias, 0.f, b, sub, lanes, chunks);
+            }
+            const F2 scale = F2(rs, rs);
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) s[0] += v[c][e];
-    row_sums<WARP>(s, lanes, sm[0]);
-    const float mu = s[0] * inv;
-    s[0] = 0.f;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        if (sub + c * lanes < chunks) {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) s[0] = fmaf(v[c][e] - mu, v[c][e] - mu, s[0]);
+            for (int i = 0; i < EPT / 2; ++i) v[i] = fma2(mul2(add2(v[i], minus), scale), w[i], b[i]);
+            Part::store(y + at, v, sub, lanes, chunks);
+            if (sub == 0) {
+                if (mean) mean[r] = mu;
+                if (rstd) rstd[r] = rs;
+            }
         }
-    }
-    row_sums<WARP>(s, lanes, sm[1]);
-    const float rs = rsqrtf(s[0] * inv + eps);
-    if (!live) return;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int i = sub + c * lanes;
-        if (i >= chunks) continue;
-        if (sum_out) V::store(sum_out + at + i * VE, v[c]);
-        float w[VE], b[VE];
-        if (weight) ln_weights<W, VE>(weight + i * VE, w);
-        if (bias) ln_weights<W, VE>(bias + i * VE, b);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            float z = (v[c][e] - mu) * rs;
-            if (weight) z *= w[e];
-            if (bias) z += b[e];
-            v[c][e] = z;
-        }
-        V::store(y + at + i * VE, v[c]);
-    }
-    if (sub == 0) {
-        if (mean) mean[r] = mu;
-        if (rstd) rstd[r] = rs;
     }
 }
 
@@ -142,12 +200,12 @@ ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const 
 // the current row's two sums are reduced. Each block ends with one row of partial sums, part
 // [gridDim.x, 2, D]; ln_reduce_kernel adds those in block order.
 template <typename T, typename W, int VE, int EPT, bool WARP>
-__global__ void __launch_bounds__(WARP ? kLnThreads : (EPT <= 8 ? 1024 : 512))
+__global__ void __launch_bounds__(WARP ? kLnThreads : 512)
 ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const float* __restrict__ mean,
                    const float* __restrict__ rstd, const T* dsum, T* dx, float* __restrict__ part, unsigned rows, int D,
                    int lanes) {
-    using V = Vec<T, VE>;
-    constexpr int CH = EPT / VE;
+    using Part = RowPart<T, VE, EPT>;
+    constexpr int P = EPT / 2;
     extern __shared__ float ln_sm[];  // WARP: [2, D] for joining the warps' column sums
     __shared__ __align__(16) float sm[2][2][32];
     const int sub = WARP ? threadIdx.x & (lanes - 1) : threadIdx.x;
@@ -155,118 +213,88 @@ ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const 
     const unsigned step = gridDim.x * per_block;
     const int chunks = D / VE;
     const float inv = 1.f / (float)D;
-    float w[CH][VE], dw[CH][VE], db[CH][VE];
+    F2 w[P], dw[P], db[P];
+    column_weights<W, VE, EPT>(weight, 1.f, w, sub, lanes, chunks);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-            w[c][e] = 1.f;
-            dw[c][e] = db[c][e] = 0.f;
-        }
-        if (weight && sub + c * lanes < chunks) ln_weights<W, VE>(weight + (sub + c * lanes) * VE, w[c]);
-    }
-    struct Row {
-        typename V::Raw g[CH], x[CH], s[CH];
-        float mu, rs;
-    };
-    auto load = [&](Row& q, unsigned r) {
-        const size_t at = (size_t)r * D;
+    for (int i = 0; i < P; ++i) dw[i] = db[i] = F2(0.f, 0.f);
+    Part dyp, xp, sp;
+    float mu, rs;
+    auto load = [&](unsigned r) {
         const bool live = r < rows;
-        q.mu = live ? mean[r] : 0.f;
-        q.rs = live ? rstd[r] : 0.f;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = sub + c * lanes;
-            q.g[c] = q.x[c] = q.s[c] = V::zero();
-            if (live && i < chunks) {
-                q.g[c] = V::load_cs(dy + at + i * VE);
-                q.x[c] = V::load_cs(x + at + i * VE);
-                if (dsum) q.s[c] = V::load_cs(dsum + at + i * VE);
-            }
-        }
+        mu = live ? mean[r] : 0.f;
+        rs = live ? rstd[r] : 0.f;
+        dyp.load(dy + (size_t)r * D, sub, lanes, chunks, live);
+        xp.load(x + (size_t)r * D, sub, lanes, chunks, live);
+        if (dsum) sp.load(dsum + (size_t)r * D, sub, lanes, chunks, live);
     };
-    Row cur;
     unsigned base = blockIdx.x * per_block;  // every thread of a block makes the same trips
-    load(cur, base + mine);
+    load(base + mine);
     for (int flip = 0; base < rows; base += step, flip ^= 1) {
         const unsigned r = base + mine;
-        Row next;
-        load(next, r + step);
-        float s[2] = {0.f, 0.f};
+        F2 u[P], xh[P], add[P];
+        dyp.pairs(u);
+        xp.pairs(xh);
+        if (dsum) sp.pairs(add);
+        const float scale = rs, shift = -mu * rs;
+        load(r + step);
+        // columns behind the row: dy is 0 there, so whatever xh holds (finite) adds nothing
+        F2 s0 = F2(0.f, 0.f), s1 = s0;
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            float g[VE], z[VE];
-            V::unpack(cur.g[c], g);
-            V::unpack(cur.x[c], z);
-            const bool on = sub + c * lanes < chunks;
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float xh = on ? (z[e] - cur.mu) * cur.rs : 0.f, u = g[e] * w[c][e];
-                s[0] += u;
-                s[1] = fmaf(u, xh, s[1]);
-                dw[c][e] = fmaf(g[e], xh, dw[c][e]);
-                db[c][e] += g[e];
-            }
+        for (int i = 0; i < P; ++i) {
+            xh[i] = fma2(xh[i], F2(scale, scale), F2(shift, shift));
+            dw[i] = fma2(u[i], xh[i], dw[i]);
+            db[i] = add2(db[i], u[i]);
+            u[i] = mul2(u[i], w[i]);
+            s0 = add2(s0, u[i]);
+            s1 = fma2(u[i], xh[i], s1);
         }
+        float s[2] = {s0.sum(), s1.sum()};
         row_sums<WARP>(s, lanes, sm[flip]);
-        const float m0 = s[0] * inv, m1 = s[1] * inv;
-        const size_t at = (size_t)r * D;
+        if (r < rows) {
+            const float m0 = -scale * (s[0] * inv), m1 = -scale * (s[1] * inv);
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = sub + c * lanes;
-            if (r >= rows || i >= chunks) continue;
-            float g[VE], z[VE], a[VE];
-            V::unpack(cur.g[c], g);
-            V::unpack(cur.x[c], z);
-            V::unpack(cur.s[c], a);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float xh = (z[e] - cur.mu) * cur.rs;
-                z[e] = cur.rs * (g[e] * w[c][e] - m0 - xh * m1) + (dsum ? a[e] : 0.f);
+            for (int i = 0; i < P; ++i) {
+                u[i] = fma2(xh[i], F2(m1, m1), fma2(u[i], F2(scale, scale), F2(m0, m0)));
+                if (dsum) u[i] = add2(u[i], add[i]);
             }
-            V::store(dx + at + i * VE, z);
+            Part::store(dx + (size_t)r * D, u, sub, lanes, chunks);
         }
-        cur = next;
     }
     if (!part) return;
     float* out = part + (size_t)blockIdx.x * 2 * D;
     if (WARP) {  // the groups of a warp, then the warps one after another
+        float* acc = ln_sm;
         for (int off = 16; off >= lanes; off >>= 1) {
 #pragma unroll
-            for (int c = 0; c < CH; ++c)
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    dw[c][e] += __shfl_xor_sync(0xffffffffu, dw[c][e], off);
-                    db[c][e] += __shfl_xor_sync(0xffffffffu, db[c][e], off);
-                }
+            for (int i = 0; i < P; ++i) {
+                F2 q;
+                q.v = __shfl_xor_sync(0xffffffffu, dw[i].v, off);
+                dw[i] = add2(dw[i], q);
+                q.v = __shfl_xor_sync(0xffffffffu, db[i].v, off);
+                db[i] = add2(db[i], q);
+            }
         }
         for (int q = 0; q < kLnThreads / 32; ++q) {
             if ((int)(threadIdx.x >> 5) == q && (threadIdx.x & 31) < lanes) {
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    const int i = sub + c * lanes;
-                    if (i >= chunks) continue;
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        float* a = ln_sm + i * VE + e;
-                        a[0] = q ? a[0] + dw[c][e] : dw[c][e];
-                        a[D] = q ? a[D] + db[c][e] : db[c][e];
-                    }
+                for (int e = 0; e < EPT; ++e) {
+                    const int i = (sub + e / VE * lanes) * VE + e % VE;
+                    if (i >= D) continue;
+                    const float a = e & 1 ? dw[e / 2].hi() : dw[e / 2].lo(), d = e & 1 ? db[e / 2].hi() : db[e / 2].lo();
+                    acc[i] = q ? acc[i] + a : a;
+                    acc[D + i] = q ? acc[D + i] + d : d;
                 }
             }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < 2 * D; c += kLnThreads) out[c] = ln_sm[c];
+        for (int c = threadIdx.x; c < 2 * D; c += kLnThreads) out[c] = acc[c];
     } else {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = sub + c * lanes;
-            if (i >= chunks) continue;
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                out[i * VE + e] = dw[c][e];
-                out[D + i * VE + e] = db[c][e];
-            }
+        for (int e = 0; e < EPT; ++e) {
+            const int i = (sub + e / VE * lanes) * VE + e % VE;
+            if (i >= D) continue;
+            out[i] = e & 1 ? dw[e / 2].hi() : dw[e / 2].lo();
+            out[D + i] = e & 1 ? db[e / 2].hi() : db[e / 2].lo();
         }
     }
 }

@@ -2,6 +2,7 @@
 // selection and launch. One translation unit holds every kernel so that they
 // share the module-scope device error word.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -612,31 +613,49 @@ inline int lanes_for(int chunks) {  // a power of two up to 32
 }
 inline int warp_threads(int n) { return (n + 31) / 32 * 32; }
 
-template <typename T, typename W, int VE, int EPT, bool WARP>
+// Blocks that stay: as many as fit the device at once, or as many as the rows need. The
+// occupancy of one instance is asked for once per block size (the devices of a machine are alike).
+template <typename Kernel>
+int staying_blocks(Kernel kernel, std::atomic<int> (&known)[33], int threads, size_t smem, long long blocks) {
+    std::atomic<int>& k = known[threads / 32];
+    int per_sm = k.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+            per_sm = 1;
+        k.store(per_sm, std::memory_order_relaxed);
+    }
+    return (int)std::min<long long>(blocks, (long long)per_sm * tc::sm_count());
+}
+
+template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD>
 ret_status launch_ln_forward(const T* x, const T* res, const W* w, const W* b, T* y, T* sum_out, float* mean,
                              float* rstd, long long rows, int D, float eps, cudaStream_t st) {
+    static std::atomic<int> known[33];
     const int chunks = D / VE;
     const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
-    const long long per_block = WARP ? kLnThreads / lanes : 1;
-    ln_forward_kernel<T, W, VE, EPT, WARP><<<(unsigned)((rows + per_block - 1) / per_block), WARP ? kLnThreads : lanes,
-                                             0, st>>>(x, res, w, b, y, sum_out, mean, rstd, (unsigned)rows, D, eps,
-                                                      lanes);
+    const int threads = WARP ? kLnThreads : lanes;
+    const long long per_block = WARP ? threads / lanes : 1;
+    const auto kernel = ln_forward_kernel<T, W, VE, EPT, WARP, HOLD>;
+    const int grid = staying_blocks(kernel, known, threads, 0, (rows + per_block - 1) / per_block);
+    kernel<<<grid, threads, 0, st>>>(x, res, w, b, y, sum_out, mean, rstd, (unsigned)rows, D, eps, lanes);
     return launch_status();
 }
 
 template <typename T, typename W, int VE>
 ret_status launch_ln_forward_width(const T* x, const T* res, const W* w, const W* b, T* y, T* sum_out, float* mean,
                                    float* rstd, long long rows, int D, float eps, cudaStream_t st) {
-    if (D <= 32 * 8) return launch_ln_forward<T, W, VE, 8, true>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
-    if (D <= 32 * 16) return launch_ln_forward<T, W, VE, 16, true>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
-    if (D <= 32 * 32) return launch_ln_forward<T, W, VE, 32, true>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
-    if (D <= 256 * 8) return launch_ln_forward<T, W, VE, 8, false>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
-    if (D <= 512 * 16) return launch_ln_forward<T, W, VE, 16, false>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
-    return launch_ln_forward<T, W, VE, 32, false>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+#define RET_LN_FORWARD(LANES, EPT, WARP, HOLD) \
+    if (D <= LANES * EPT)                      \
+    return launch_ln_forward<T, W, VE, EPT, WARP, HOLD>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st)
+    RET_LN_FORWARD(32, 8, true, true);
+    RET_LN_FORWARD(32, 16, true, true);
+    RET_LN_FORWARD(512, 16, false, true);
+#undef RET_LN_FORWARD
+    return launch_ln_forward<T, W, VE, 32, false, false>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
 }
 
-// Rows in registers up to 32,768 elements, in 16-byte vectors where every row starts on 16 bytes,
-// else element by element; longer rows (and 2^31 rows and more) in three passes.
+// Rows in registers up to 16,384 elements, in 16-byte vectors where every row starts on 16 bytes,
+// else element by element; longer rows (and 2^30 rows and more) in three passes.
 template <typename T, typename W>
 ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, const void* b_, void* y_,
                              void* sum_out_, float* mean, float* rstd, long long rows, int D, float eps,
@@ -645,7 +664,7 @@ ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, c
     const T *x = static_cast<const T*>(x_), *res = static_cast<const T*>(res_);
     const W *w = static_cast<const W*>(w_), *b = static_cast<const W*>(b_);
     T *y = static_cast<T*>(y_), *sum_out = static_cast<T*>(sum_out_);
-    if (D <= 32 * 1024 && rows < (1LL << 31)) {
+    if (D <= 512 * 32 && rows < (1LL << 30)) {
         if (D % kE == 0 && aligned16(x) && aligned16(res) && aligned16(w) && aligned16(b) && aligned16(y) &&
             aligned16(sum_out))
             return launch_ln_forward_width<T, W, kE>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
@@ -657,32 +676,23 @@ ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, c
 }
 
 template <typename T, typename W, int VE, int EPT, bool WARP>
-int ln_backward_grid(long long rows, int lanes, int threads, size_t smem) {
-    int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, ln_backward_kernel<T, W, VE, EPT, WARP>, threads,
-                                                      smem) != cudaSuccess || per_sm < 1)
-        per_sm = 1;
-    const long long per_block = WARP ? threads / lanes : 1;
-    return (int)std::min<long long>((rows + per_block - 1) / per_block, (long long)per_sm * tc::sm_count());
-}
-
-// One pass over dy and x. Returns the number of partial rows that it leaves in *part (allocated here).
-template <typename T, typename W, int VE, int EPT, bool WARP>
 ret_status launch_ln_backward(const T* dy, const T* x, const W* w, const float* mean, const float* rstd, const T* dsum,
                               T* dx, W* dw, W* db, long long rows, int D, cudaStream_t st) {
     const int chunks = D / VE;
     const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
     const int threads = WARP ? kLnThreads : lanes;
     const size_t smem = WARP ? sizeof(float) * 2 * D : 0;
-    const int grid = ln_backward_grid<T, W, VE, EPT, WARP>(rows, lanes, threads, smem);
+    const long long per_block = WARP ? threads / lanes : 1;
+    static std::atomic<int> known[33];
+    const auto kernel = ln_backward_kernel<T, W, VE, EPT, WARP>;
+    const int grid = staying_blocks(kernel, known, threads, smem, (rows + per_block - 1) / per_block);
     float* part = nullptr;
     if (dw || db) {
         tc::keep_pool_memory();
         if (cudaMallocAsync(reinterpret_cast<void**>(&part), sizeof(float) * 2 * (size_t)grid * D, st) != cudaSuccess)
             return RET_ERR_CUDA;
     }
-    ln_backward_kernel<T, W, VE, EPT, WARP><<<grid, threads, smem, st>>>(dy, x, w, mean, rstd, dsum, dx, part,
-                                                                        (unsigned)rows, D, lanes);
+    kernel<<<grid, threads, smem, st>>>(dy, x, w, mean, rstd, dsum, dx, part, (unsigned)rows, D, lanes);
     ret_status r = launch_status();
     if (part) {
         if (r == RET_OK) {
