@@ -56,20 +56,62 @@ struct Vec {
         return r;
     }
     static __device__ __forceinline__ void unpack(const Raw& u, float* f) {
-        T e[VE];
-        memcpy(e, &u, sizeof(u));
+        if constexpr (sizeof(T) == 2 && VE > 1) {
+            // a bf16 is the upper half of its fp32 value: one shift or one mask per element
+            unsigned int w[VE / 2];
+            memcpy(w, &u, sizeof(u));
 #pragma unroll
-        for (int i = 0; i < VE; ++i) f[i] = ld_elem(e + i);
+            for (int i = 0; i < VE / 2; ++i) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+            T e[VE];
+            memcpy(e, &u, sizeof(u));
+#pragma unroll
+            for (int i = 0; i < VE; ++i) f[i] = ld_elem(e + i);
+        }
     }
     static __device__ __forceinline__ void store(T* p, const float* f) {
-        T e[VE];
-#pragma unroll
-        for (int i = 0; i < VE; ++i) st_elem(e + i, f[i]);
         Raw r;
-        memcpy(&r, e, sizeof(r));
+        if constexpr (sizeof(T) == 2 && VE > 1) {
+            unsigned int w[VE / 2];
+#pragma unroll
+            for (int i = 0; i < VE / 2; ++i) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+                memcpy(&w[i], &b, 4);
+            }
+            memcpy(&r, w, sizeof(r));
+        } else {
+            T e[VE];
+#pragma unroll
+            for (int i = 0; i < VE; ++i) st_elem(e + i, f[i]);
+            memcpy(&r, e, sizeof(r));
+        }
         *reinterpret_cast<Raw*>(p) = r;
     }
 };
+
+// One asynchronous copy of BYTES (4, 8 or 16) from global to shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    const unsigned at = (unsigned)__cvta_generic_to_shared(to);
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the newest LEFT groups of this thread's copies have landed (in the thread's own view).
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Programmatic dependent launch: a kernel launched with the attribute waits here for the one
+// before it in the stream, and may let the next one's blocks be placed early.
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Two floats that one instruction adds, multiplies or fuses (fma.rn.f32x2 and its kin, sm_100):
 // each half is rounded as the scalar operation rounds it.

@@ -15,6 +15,7 @@
 namespace ret {
 
 constexpr int kLnThreads = 256;
+constexpr int kLnMaxShared = 220 * 1024;  // of a block: what its rows in flight may take
 
 // VE weights as floats (vector path: the pointer is aligned to the vector, at most 16 bytes).
 template <typename W, int VE>
@@ -24,63 +25,206 @@ __device__ __forceinline__ void ln_weights(const W* w, float* f) {
     for (int e = 0; e < VE; e += kPart) Vec<W, kPart>::unpack(Vec<W, kPart>::load(w + e), f + e);
 }
 
-// A row's threads: `lanes` lanes of a warp (a power of two), or the whole block. The sums of K
-// values over them, in every one of them; sm (block form) holds K rows of 32 and is not reused
-// before the next barrier.
-template <bool WARP, int K>
-__device__ __forceinline__ void row_sums(float (&v)[K], int lanes, float (*sm)[32]) {
-    for (int off = WARP ? lanes >> 1 : 16; off > 0; off >>= 1) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
+// A row's threads: `lanes` lanes of a warp (WARP; a power of two), or `lanes` / 32 whole warps, up
+// to 16; a block holds `groups` of them, each with a row of its own. row_sum adds a value over a
+// row's threads, row_sums two at once; every thread gets the sums. Whole warps meet at a barrier of their
+// group (number group + 1) and take `sm`, one float per warp and value, zero behind the group's
+// warps and not written again before the group's next barrier.
+struct RowThreads {
+    int sub, lanes, group, groups;
+    __device__ __forceinline__ void meet() const {
+        if (groups == 1) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(lanes) : "memory");
     }
-    if (!WARP) {
-        const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-        if ((threadIdx.x & 31) < K) {
-            float mine = v[0];
+};
+constexpr int kLnWarps = 16;   // most warps of a row
+constexpr int kLnGroups = 8;   // most groups of whole warps in a block
+using RowShared = float[2][kLnWarps];
+
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+    for (int off = lanes >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
-            for (int k = 1; k < K; ++k) mine = (threadIdx.x & 31) == k ? v[k] : mine;
-            sm[threadIdx.x & 31][warp] = mine;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            float t = 0.f;
-            for (int i = 0; i < warps; i += 4) {
-                const float4 q = *reinterpret_cast<const float4*>(&sm[k][i]);
-                t += q.x;
-                if (i + 1 < warps) t += q.y;
-                if (i + 2 < warps) t += q.z;
-                if (i + 3 < warps) t += q.w;
-            }
-            v[k] = t;
-        }
-    }
+    for (int off = LANES >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
 }
 
-// A thread's EPT elements of a row: vectors sub, sub + lanes, ... of VE elements, as they are in
-// memory, and as pairs of floats.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, const RowThreads& t, RowShared& sm) {
+    if (WARP) return lanes_sum(v, t.lanes);
+    v = lanes_sum<32>(v);
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) sm[0][t.sub >> 5] = v;
+    __syncthreads();
+    return lanes_sum<kLnWarps>(sm[0][lane & (kLnWarps - 1)]);
+}
+
+// Two sums for little more than the shuffles of one: after the first exchange the lower half of
+// a warp carries a and the upper half b.
+template <bool WARP>
+__device__ __forceinline__ void row_sums(float& a, float& b, const RowThreads& t, RowShared& sm) {
+    if (WARP && t.lanes < 32) {
+        a = lanes_sum(a, t.lanes);
+        b = lanes_sum(b, t.lanes);
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const bool upper = lane >= 16;
+    float v = upper ? b : a;
+    v += __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+    v = lanes_sum<16>(v);
+    if (!WARP) {
+        if ((lane & 15) == 0) sm[upper][t.sub >> 5] = v;
+        t.meet();
+        v = lanes_sum<kLnWarps>(sm[upper][lane & (kLnWarps - 1)]);
+    }
+    const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+    a = upper ? other : v;
+    b = upper ? v : other;
+}
+
+__device__ __forceinline__ RowThreads row_threads(int lanes) {
+    RowThreads t;
+    t.lanes = lanes;
+    t.groups = blockDim.x / lanes;
+    t.group = t.groups == 1 ? 0 : threadIdx.x / lanes;
+    t.sub = threadIdx.x - t.group * lanes;
+    return t;
+}
+
+// A thread's EPT elements of a row: vectors sub, sub + lanes, ... of VE elements.
 template <typename T, int VE, int EPT>
 struct RowPart {
     using V = Vec<T, VE>;
+    using Raw = typename V::Raw;
     static constexpr int CH = EPT / VE;
-    typename V::Raw q[CH];
 
-    __device__ __forceinline__ void load(const T* row, int sub, int lanes, int chunks, bool live) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-            const int i = sub + c * lanes;
-            q[c] = V::zero();
-            if (live && i < chunks) q[c] = V::load_cs(row + i * VE);
-        }
-    }
-    __device__ __forceinline__ void pairs(F2 (&f)[EPT / 2]) const {
+    static __device__ __forceinline__ void pairs(const Raw (&q)[CH], F2 (&f)[EPT / 2]) {
         float e[EPT];
 #pragma unroll
         for (int c = 0; c < CH; ++c) V::unpack(q[c], e + c * VE);
 #pragma unroll
         for (int i = 0; i < EPT / 2; ++i) f[i] = F2(e[2 * i], e[2 * i + 1]);
     }
-    static __device__ __forceinline__ void store(T* row, const F2 (&f)[EPT / 2], int sub, int lanes, int chunks) {
+};
+
+// The rows that a thread works through: `row`, row + step, ... below `rows`, kAhead of them in
+// flight. Each thread copies its own parts of N tensors' rows (and N_STAT floats per row) into
+// slots of shared memory that no other thread reads, so it waits for its own copies alone, and
+// registers hold no row in flight but its statistics, which are loaded two rows ahead. 2-byte accesses
+// have no asynchronous copy: those wait in registers, one row ahead. Vectors behind the row read as zero; rows behind the last one are
+// not copied, and taking one gives whatever an earlier row left.
+template <typename T, int VE, int EPT, int N, int N_STAT>
+struct RowStream {
+    using Part = RowPart<T, VE, EPT>;
+    using Raw = typename Part::Raw;
+    static constexpr int CH = Part::CH;
+    static constexpr bool kAsync = sizeof(Raw) >= 4;
+    // rows in slots: four of up to 64 bytes per thread, three of up to 128, two of more
+    static constexpr int kRowBytes = N * CH * (int)sizeof(Raw);
+    static constexpr int kSlots = !kAsync ? 0 : kRowBytes <= 64 ? 4 : kRowBytes <= 128 ? 3 : 2;
+    static constexpr int kAhead = kAsync ? kSlots - 1 : 1;
+    // [slot][tensor][vector][thread]: neighbouring threads' copies lie side by side (a thread's own slots side by side, threads an odd number
+    // of 16-byte units apart, was a third slower: fp32 8192 x 2048 forward 32.4 us against 24.3 us)
+    static constexpr size_t bytes(int threads) { return (size_t)kSlots * threads * kRowBytes; }
+
+    const T* src[N];  // of this thread's first vector of the next row to copy
+    const float* stat[N_STAT > 0 ? N_STAT : 1];
+    unsigned next, step, rows;  // the next row to copy
+    long long stride;           // elements from a row to the next of this thread
+    int gap;                    // elements from a vector to the next of this thread
+    bool has[CH];
+    unsigned char* slots;          // this thread's place in slot 0
+    int put, get;                  // the slot to fill and the slot to read next
+    int pitch;                     // bytes from a vector to the thread's next
+    Raw held[kAsync ? 1 : N][CH];
+    float stats[2][N_STAT > 0 ? N_STAT : 1];  // of the current row and the next
+    unsigned next_stat;
+
+    __device__ __forceinline__ void issue() {
+        if (next < rows) {
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    if (!has[c]) continue;
+                    if (kAsync) copy_async<kAsync ? (int)sizeof(Raw) : 4>(slots + (put * N * CH + t * CH + c) * pitch, src[t] + c * gap);
+                    else held[kAsync ? 0 : t][c] = Part::V::load_cs(src[t] + c * gap);
+                }
+                src[t] += stride;
+            }
+            next += step;
+        }
+        if (kAsync) {
+            copy_commit();
+            put = put == kSlots - 1 ? 0 : put + 1;
+        }
+    }
+    __device__ __forceinline__ void load_stats(float (&s)[N_STAT > 0 ? N_STAT : 1]) {
+#pragma unroll
+        for (int k = 0; k < N_STAT; ++k) s[k] = next_stat < rows ? __ldg(stat[k] + next_stat) : 0.f;
+        next_stat += step;
+    }
+    // src and stat are set; issues the first kAhead rows
+    __device__ __forceinline__ void start(void* smem, const RowThreads& t, unsigned row, unsigned step_, unsigned rows_,
+                                          int D) {
+        const int chunks = D / VE;
+        next = row;
+        step = step_;
+        rows = rows_;
+        stride = (long long)step * D;
+        gap = t.lanes * VE;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            src[k] += row < rows ? (size_t)row * D + t.sub * VE : 0;
+        }
+        pitch = blockDim.x * (int)sizeof(Raw);
+        slots = static_cast<unsigned char*>(smem) + threadIdx.x * sizeof(Raw);
+        next_stat = row;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) load_stats(stats[k]);
+        put = get = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            has[c] = t.sub + c * t.lanes < chunks;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                if (!kAsync) held[kAsync ? 0 : k][c] = Part::V::zero();
+                else if (!has[c])
+                    for (int q = 0; q < kSlots; ++q)
+                        *reinterpret_cast<Raw*>(slots + (q * N * CH + k * CH + c) * pitch) = Part::V::zero();
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) issue();
+    }
+    // the current row's parts; then the row that its slot's turn comes to is issued
+    __device__ __forceinline__ void take(F2 (&f)[N][EPT / 2], float (&s)[N_STAT > 0 ? N_STAT : 1]) {
+        if (N_STAT > 0) {
+#pragma unroll
+            for (int k = 0; k < N_STAT; ++k) {
+                s[k] = stats[0][k];
+                stats[0][k] = stats[1][k];
+            }
+            load_stats(stats[1]);
+        }
+        if (kAsync) copy_wait<kAhead - 1>();
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            Raw q[CH];
+#pragma unroll
+            for (int c = 0; c < CH; ++c) q[c] = kAsync ? *reinterpret_cast<const Raw*>(slots + (get * N * CH + t * CH + c) * pitch) : held[kAsync ? 0 : t][c];
+            Part::pairs(q, f[t]);
+        }
+        if (kAsync) {
+            get = get == kSlots - 1 ? 0 : get + 1;
+        }
+        issue();
+    }
+    __device__ __forceinline__ void store(T* row, const F2 (&f)[EPT / 2]) const {  // row: this thread's first vector
         float e[EPT];
 #pragma unroll
         for (int i = 0; i < EPT / 2; ++i) {
@@ -89,8 +233,7 @@ struct RowPart {
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int i = sub + c * lanes;
-            if (i < chunks) V::store(row + i * VE, e + c * VE);
+            if (has[c]) Part::V::store(row + c * gap, e + c * VE);
         }
     }
 };
@@ -116,78 +259,67 @@ __device__ __forceinline__ void column_weights(const W* w, float none, F2 (&f)[E
 // stay and take every gridDim.x-th row; the next row's loads are issued before the current
 // row's sums are reduced. HOLD: the thread's columns of weight and bias stay in registers too, else they
 // are read from L1 for every row.
-template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD>
+template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD, bool RES>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
 ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const W* __restrict__ bias, T* y, T* sum_out,
                   float* __restrict__ mean, float* __restrict__ rstd, unsigned rows, int D, float eps, int lanes) {
-    using Part = RowPart<T, VE, EPT>;
-    __shared__ __align__(16) float sm[2][2][1][32];
-    const int sub = WARP ? threadIdx.x & (lanes - 1) : threadIdx.x;
-    const unsigned per_block = WARP ? kLnThreads / lanes : 1, mine = WARP ? threadIdx.x / lanes : 0;
-    const unsigned step = gridDim.x * per_block;
-    const int chunks = D / VE;
+    extern __shared__ uint4 ln_ring[];
+    __shared__ RowShared sm[2][2];  // one group of whole warps
+    const RowThreads t = row_threads(lanes);
+    const unsigned per_block = t.groups, mine = t.group, step = gridDim.x * per_block;
     const float inv = 1.f / (float)D;
+    if (!WARP) {
+        for (int i = t.sub; i < 4 * 2 * kLnWarps; i += lanes) (&sm[0][0][0][0])[i] = 0.f;
+    }
+    wait_previous_kernel();
+    unsigned base = blockIdx.x * per_block;  // every group of a block makes the same trips
+    RowStream<T, VE, EPT, RES ? 2 : 1, 0> in;
+    in.src[0] = x;
+    if (RES) in.src[RES] = res;
+    in.start(ln_ring, t, base + mine, step, rows, D);
+    size_t at = (size_t)(base + mine) * D + t.sub * VE;
     F2 w[EPT / 2], b[EPT / 2];
     if (HOLD) {
-        column_weights<W, VE, EPT>(weight, 1.f, w, sub, lanes, chunks);
-        column_weights<W, VE, EPT>(bias, 0.f, b, sub, lanes, chunks);
+        column_weights<W, VE, EPT>(weight, 1.f, w, t.sub, lanes, D / VE);
+        column_weights<W, VE, EPT>(bias, 0.f, b, t.sub, lanes, D / VE);
     }
-    Part cur, cur_res;
-    unsigned base = blockIdx.x * per_block;  // every thread of a block makes the same trips
-    auto load = [&](Part& p, Part& pr, unsigned r) {
-        p.load(x + (size_t)r * D, sub, lanes, chunks, r < rows);
-        if (res) pr.load(res + (size_t)r * D, sub, lanes, chunks, r < rows);
-    };
-    load(cur, cur_res, base + mine);
-    for (int flip = 0; base < rows; base += step, flip ^= 1) {
+    if (!WARP) __syncthreads();
+    for (int flip = 0; base < rows; base += step, at += in.stride, flip ^= 1) {
         const unsigned r = base + mine;
-        F2 v[EPT / 2];
-        cur.pairs(v);
-        if (res) {
-            F2 f[EPT / 2];
-            cur_res.pairs(f);
+        F2 f[RES ? 2 : 1][EPT / 2];
+        float none[1];
+        in.take(f, none);
+        F2(&v)[EPT / 2] = f[0];
+        if (RES) {
 #pragma unroll
-            for (int i = 0; i < EPT / 2; ++i) v[i] = add2(v[i], f[i]);
+            for (int i = 0; i < EPT / 2; ++i) v[i] = add2(v[i], f[RES][i]);
         }
-        load(cur, cur_res, r + step);
-        F2 t = v[0];
+        F2 q = v[0];
 #pragma unroll
-        for (int i = 1; i < EPT / 2; ++i) t = add2(t, v[i]);
-        float s[1] = {t.sum()};
-        row_sums<WARP>(s, lanes, sm[flip][0]);
-        const float mu = s[0] * inv;
+        for (int i = 1; i < EPT / 2; ++i) q = add2(q, v[i]);
+        const float mu = row_sum<WARP>(q.sum(), t, sm[flip][0]) * inv;
         const F2 minus = F2(-mu, -mu);
-        t = F2(0.f, 0.f);
+        q = F2(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < Part::CH; ++c) {
-            if (sub + c * lanes < chunks) {
-                if (VE == 1) {
-                    const float z = (c & 1 ? v[c / 2].hi() : v[c / 2].lo()) - mu;
-                    t = add2(t, F2(z * z, 0.f));
-                } else {
-#pragma unroll
-                    for (int i = c * VE / 2; i < (c + 1) * VE / 2; ++i) {
-                        const F2 z = add2(v[i], minus);
-                        t = fma2(z, z, t);
-                    }
-                }
-            }
+        for (int i = 0; i < EPT / 2; ++i) {
+            // elements behind the row stay out of the sum of centred squares
+            const F2 z = VE > 1 ? (in.has[2 * i / VE] ? add2(v[i], minus) : F2(0.f, 0.f))
+                                : F2(in.has[2 * i / VE] ? v[i].lo() - mu : 0.f,
+                                     in.has[(2 * i + 1) / VE] ? v[i].hi() - mu : 0.f);
+            q = fma2(z, z, q);
         }
-        s[0] = t.sum();
-        row_sums<WARP>(s, lanes, sm[flip][1]);
-        const float rs = rsqrtf(s[0] * inv + eps);
+        const float rs = rsqrtf(row_sum<WARP>(q.sum(), t, sm[flip][1]) * inv + eps);
         if (r < rows) {
-            const size_t at = (size_t)r * D;
-            if (sum_out) Part::store(sum_out + at, v, sub, lanes, chunks);
+            if (RES && sum_out) in.store(sum_out + at, v);
             if (!HOLD) {
-                column_weights<W, VE, EPT>(weight, 1.f, w, sub, lanes, chunks);
-                column_weights<W, VE, EPT>(bias, 0.f, b, sub, lanes, chunks);
+                column_weights<W, VE, EPT>(weight, 1.f, w, t.sub, lanes, D / VE);
+                column_weights<W, VE, EPT>(bias, 0.f, b, t.sub, lanes, D / VE);
             }
             const F2 scale = F2(rs, rs);
 #pragma unroll
             for (int i = 0; i < EPT / 2; ++i) v[i] = fma2(mul2(add2(v[i], minus), scale), w[i], b[i]);
-            Part::store(y + at, v, sub, lanes, chunks);
-            if (sub == 0) {
+            in.store(y + at, v);
+            if (t.sub == 0) {
                 if (mean) mean[r] = mu;
                 if (rstd) rstd[r] = rs;
             }
@@ -198,72 +330,81 @@ ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const 
 // dx and the column sums in one pass: blocks stay, and a thread keeps the same EPT columns of
 // every row it takes, their dw and db sums in registers. The next row's loads are issued before
 // the current row's two sums are reduced. Each block ends with one row of partial sums, part
-// [gridDim.x, 2, D]; ln_reduce_kernel adds those in block order.
-template <typename T, typename W, int VE, int EPT, bool WARP>
+// [gridDim.x, 2, ln_pitch(D)]; ln_reduce_kernel adds those in order.
+__host__ __device__ constexpr int ln_pitch(int D) { return (D + 3) / 4 * 4; }
+
+template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
 ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const float* __restrict__ mean,
                    const float* __restrict__ rstd, const T* dsum, T* dx, float* __restrict__ part, unsigned rows, int D,
                    int lanes) {
-    using Part = RowPart<T, VE, EPT>;
     constexpr int P = EPT / 2;
-    extern __shared__ float ln_sm[];  // WARP: [2, D] for joining the warps' column sums
-    __shared__ __align__(16) float sm[2][2][32];
-    const int sub = WARP ? threadIdx.x & (lanes - 1) : threadIdx.x;
-    const unsigned per_block = WARP ? kLnThreads / lanes : 1, mine = WARP ? threadIdx.x / lanes : 0;
-    const unsigned step = gridDim.x * per_block;
-    const int chunks = D / VE;
+    extern __shared__ uint4 ln_ring[];  // rows in flight, and at the end column sums
+    __shared__ RowShared sm_all[WARP ? 1 : kLnGroups][2];
+    const RowThreads t = row_threads(lanes);
+    RowShared(&sm)[2] = sm_all[WARP ? 0 : t.group];
+    const int sub = t.sub;
+    const unsigned per_block = t.groups, mine = t.group, step = gridDim.x * per_block;
     const float inv = 1.f / (float)D;
+    if (!WARP) {
+        for (int i = t.sub; i < 2 * 2 * kLnWarps; i += lanes) (&sm[0][0][0])[i] = 0.f;
+    }
+    allow_next_kernel();
+    wait_previous_kernel();
+    unsigned base = blockIdx.x * per_block;  // every group of a block makes the same trips
+    RowStream<T, VE, EPT, SUM ? 3 : 2, 2> in;
+    in.src[0] = dy;
+    in.src[1] = x;
+    if (SUM) in.src[SUM ? 2 : 0] = dsum;
+    in.stat[0] = mean;
+    in.stat[1] = rstd;
+    in.start(ln_ring, t, base + mine, step, rows, D);
+    size_t at = (size_t)(base + mine) * D + sub * VE;
     F2 w[P], dw[P], db[P];
-    column_weights<W, VE, EPT>(weight, 1.f, w, sub, lanes, chunks);
+    column_weights<W, VE, EPT>(weight, 1.f, w, sub, lanes, D / VE);
 #pragma unroll
     for (int i = 0; i < P; ++i) dw[i] = db[i] = F2(0.f, 0.f);
-    Part dyp, xp, sp;
-    float mu, rs;
-    auto load = [&](unsigned r) {
-        const bool live = r < rows;
-        mu = live ? mean[r] : 0.f;
-        rs = live ? rstd[r] : 0.f;
-        dyp.load(dy + (size_t)r * D, sub, lanes, chunks, live);
-        xp.load(x + (size_t)r * D, sub, lanes, chunks, live);
-        if (dsum) sp.load(dsum + (size_t)r * D, sub, lanes, chunks, live);
-    };
-    unsigned base = blockIdx.x * per_block;  // every thread of a block makes the same trips
-    load(base + mine);
-    for (int flip = 0; base < rows; base += step, flip ^= 1) {
+    if (!WARP) t.meet();
+    for (int flip = 0; base < rows; base += step, at += in.stride, flip ^= 1) {
         const unsigned r = base + mine;
-        F2 u[P], xh[P], add[P];
-        dyp.pairs(u);
-        xp.pairs(xh);
-        if (dsum) sp.pairs(add);
-        const float scale = rs, shift = -mu * rs;
-        load(r + step);
+        F2 f[SUM ? 3 : 2][P];
+        float st[2];
+        in.take(f, st);
+        F2(&u)[P] = f[0];
+        F2(&xh)[P] = f[1];
+        const float scale = st[1], shift = -st[0] * st[1];
         // columns behind the row: dy is 0 there, so whatever xh holds (finite) adds nothing
         F2 s0 = F2(0.f, 0.f), s1 = s0;
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            xh[i] = fma2(xh[i], F2(scale, scale), F2(shift, shift));
-            dw[i] = fma2(u[i], xh[i], dw[i]);
-            db[i] = add2(db[i], u[i]);
-            u[i] = mul2(u[i], w[i]);
-            s0 = add2(s0, u[i]);
-            s1 = fma2(u[i], xh[i], s1);
-        }
-        float s[2] = {s0.sum(), s1.sum()};
-        row_sums<WARP>(s, lanes, sm[flip]);
         if (r < rows) {
-            const float m0 = -scale * (s[0] * inv), m1 = -scale * (s[1] * inv);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                xh[i] = fma2(xh[i], F2(scale, scale), F2(shift, shift));
+                dw[i] = fma2(u[i], xh[i], dw[i]);
+                db[i] = add2(db[i], u[i]);
+                u[i] = mul2(u[i], w[i]);
+                s0 = add2(s0, u[i]);
+                s1 = fma2(u[i], xh[i], s1);
+            }
+        }
+        float a = s0.sum(), c = s1.sum();
+        row_sums<WARP>(a, c, t, sm[flip]);
+        if (r < rows) {
+            const float m0 = -scale * (a * inv), m1 = -scale * (c * inv);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 u[i] = fma2(xh[i], F2(m1, m1), fma2(u[i], F2(scale, scale), F2(m0, m0)));
-                if (dsum) u[i] = add2(u[i], add[i]);
+                if (SUM) u[i] = add2(u[i], f[SUM ? 2 : 0][i]);
             }
-            Part::store(dx + (size_t)r * D, u, sub, lanes, chunks);
+            in.store(dx + at, u);
         }
     }
     if (!part) return;
-    float* out = part + (size_t)blockIdx.x * 2 * D;
-    if (WARP) {  // the groups of a warp, then the warps one after another
-        float* acc = ln_sm;
+    // column sums to shared memory, [2, Dp]: the groups of a warp (WARP) joined first, then one warp or
+    // group after another
+    __syncthreads();  // no copy is in flight: every row that was issued has been taken
+    float* acc = reinterpret_cast<float*>(ln_ring);
+    const int Dp = ln_pitch(D);
+    if (WARP) {
         for (int off = 16; off >= lanes; off >>= 1) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -274,29 +415,26 @@ ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const 
                 db[i] = add2(db[i], q);
             }
         }
-        for (int q = 0; q < kLnThreads / 32; ++q) {
-            if ((int)(threadIdx.x >> 5) == q && (threadIdx.x & 31) < lanes) {
+    }
+    const int turn = WARP ? threadIdx.x >> 5 : t.group, turns = WARP ? kLnThreads / 32 : t.groups;
+    for (int q = 0; q < turns; ++q) {
+        if (turn == q && (!WARP || (int)(threadIdx.x & 31) < lanes)) {
 #pragma unroll
-                for (int e = 0; e < EPT; ++e) {
-                    const int i = (sub + e / VE * lanes) * VE + e % VE;
-                    if (i >= D) continue;
-                    const float a = e & 1 ? dw[e / 2].hi() : dw[e / 2].lo(), d = e & 1 ? db[e / 2].hi() : db[e / 2].lo();
-                    acc[i] = q ? acc[i] + a : a;
-                    acc[D + i] = q ? acc[D + i] + d : d;
+            for (int i = 0; i < P; ++i) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int e = 2 * i + k, at_col = (sub + e / VE * lanes) * VE + e % VE;
+                    if (!in.has[e / VE]) continue;
+                    const float a = k ? dw[i].hi() : dw[i].lo(), d = k ? db[i].hi() : db[i].lo();
+                    acc[at_col] = q ? acc[at_col] + a : a;
+                    acc[Dp + at_col] = q ? acc[Dp + at_col] + d : d;
                 }
             }
-            __syncthreads();
         }
-        for (int c = threadIdx.x; c < 2 * D; c += kLnThreads) out[c] = acc[c];
-    } else {
-#pragma unroll
-        for (int e = 0; e < EPT; ++e) {
-            const int i = (sub + e / VE * lanes) * VE + e % VE;
-            if (i >= D) continue;
-            out[i] = e & 1 ? dw[e / 2].hi() : dw[e / 2].lo();
-            out[D + i] = e & 1 ? db[e / 2].hi() : db[e / 2].lo();
-        }
+        __syncthreads();
     }
+    float4* out = reinterpret_cast<float4*>(part + (size_t)blockIdx.x * 2 * Dp);
+    for (int q = threadIdx.x; q < Dp / 2; q += blockDim.x) out[q] = reinterpret_cast<const float4*>(acc)[q];
 }
 
 // Sum over the block, in every thread. `sm` holds one float per warp and may be reused at once.
@@ -370,7 +508,7 @@ ln_backward_rows_kernel(const T* dy, const T* x, const W* __restrict__ weight, c
 }
 
 // Partial sums of dw and db over every gridDim.y-th row, one column per thread, in
-// part [gridDim.y, 2, D]; ln_reduce_kernel adds them in row order, so calls agree bit for bit.
+// part [gridDim.y, 2, ln_pitch(D)].
 template <typename T>
 __global__ void __launch_bounds__(kLnThreads)
 ln_backward_columns_kernel(const T* __restrict__ dy, const T* __restrict__ x, const float* __restrict__ mean,
@@ -383,32 +521,42 @@ ln_backward_columns_kernel(const T* __restrict__ dy, const T* __restrict__ x, co
         dw = fmaf(g, (ld_elem(x + r * D + c) - mean[r]) * rstd[r], dw);
         db += g;
     }
-    part[(size_t)blockIdx.y * 2 * D + c] = dw;
-    part[((size_t)blockIdx.y * 2 + 1) * D + c] = db;
+    part[(size_t)blockIdx.y * 2 * ln_pitch(D) + c] = dw;
+    part[((size_t)blockIdx.y * 2 + 1) * ln_pitch(D) + c] = db;
 }
 
-// dw and db from `parts` rows of partial sums [2, D]: 32 columns per block, eight threads per
-// column over every eighth row, then those eight one after another.
-constexpr int kReduceSlices = kLnThreads / 32;
+// dw and db from `parts` rows of partial sums: 16 columns per block, four per thread, 64 threads per
+// column over every 64th row; those are joined in a fixed order, so calls agree bit for bit.
+constexpr int kReduceColumns = 16, kReduceQuads = kReduceColumns / 4;
 template <typename W>
 __global__ void __launch_bounds__(kLnThreads)
 ln_reduce_kernel(const float* __restrict__ part, int parts, W* __restrict__ dweight, W* __restrict__ dbias, int D) {
-    __shared__ float sm[kReduceSlices][32];
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const long long c = blockIdx.x * 32LL + lane;  // of 2 D
-    float t = 0.f;
-    if (c < 2LL * D) {
-#pragma unroll 8
-        for (int p = slice; p < parts; p += kReduceSlices) t += part[(size_t)p * 2 * D + c];
+    __shared__ float4 sm[kLnThreads / 32][kReduceQuads];
+    const int Dp = ln_pitch(D), quad = threadIdx.x % kReduceQuads, slice = threadIdx.x / kReduceQuads;
+    const int c = blockIdx.x * kReduceColumns + 4 * quad;  // of 2 Dp
+    wait_previous_kernel();
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float4& z) { t = make_float4(t.x + z.x, t.y + z.y, t.z + z.z, t.w + z.w); };
+    if (c < 2 * Dp) {
+#pragma unroll 4
+        for (int p = slice; p < parts; p += kLnThreads / kReduceQuads)
+            add(__ldcg(reinterpret_cast<const float4*>(part + (size_t)p * 2 * Dp + c)));
     }
-    sm[slice][lane] = t;
-    __syncthreads();
-    if (slice == 0 && c < 2LL * D) {
 #pragma unroll
-        for (int i = 1; i < kReduceSlices; ++i) t += sm[i][lane];
-        W* out = c < D ? dweight : dbias;
-        if (out) st_elem(out + (c < D ? c : c - D), t);
+    for (int off = kReduceQuads; off < 32; off <<= 1) {
+        add(make_float4(__shfl_xor_sync(0xffffffffu, t.x, off), __shfl_xor_sync(0xffffffffu, t.y, off),
+                        __shfl_xor_sync(0xffffffffu, t.z, off), __shfl_xor_sync(0xffffffffu, t.w, off)));
     }
+    if ((threadIdx.x & 31) < kReduceQuads) sm[threadIdx.x >> 5][quad] = t;
+    __syncthreads();
+    const int mine = blockIdx.x * kReduceColumns + threadIdx.x;
+    if (threadIdx.x >= kReduceColumns || mine >= 2 * Dp) return;
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLnThreads / 32; ++i) v += reinterpret_cast<const float*>(sm[i])[threadIdx.x];
+    const int col = mine < Dp ? mine : mine - Dp;
+    W* out = mine < Dp ? dweight : dbias;
+    if (out && col < D) st_elem(out + col, v);
 }
 
 }  // namespace ret

@@ -613,49 +613,60 @@ inline int lanes_for(int chunks) {  // a power of two up to 32
 }
 inline int warp_threads(int n) { return (n + 31) / 32 * 32; }
 
-// Blocks that stay: as many as fit the device at once, or as many as the rows need. The
-// occupancy of one instance is asked for once per block size (the devices of a machine are alike).
+// Blocks that stay: as many as fit the device at once, or as many as the rows need. A kernel's
+// occupancy (its shared memory limit raised first) is asked for once per device and block size.
+struct StayingBlocks {
+    std::atomic<int> per_sm[kMaxDevices][17];
+};
 template <typename Kernel>
-int staying_blocks(Kernel kernel, std::atomic<int> (&known)[33], int threads, size_t smem, long long blocks) {
-    std::atomic<int>& k = known[threads / 32];
-    int per_sm = k.load(std::memory_order_relaxed);
+int staying_blocks(Kernel kernel, StayingBlocks& known, int threads, size_t smem, long long blocks) {
+    const int dev = tc::current_device();
+    std::atomic<int>* k = dev >= 0 && dev < kMaxDevices ? &known.per_sm[dev][threads / 32] : nullptr;
+    int per_sm = k ? k->load(std::memory_order_relaxed) : 0;
     if (per_sm == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
-            per_sm = 1;
-        k.store(per_sm, std::memory_order_relaxed);
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLnMaxShared) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+            return 0;
+        if (k) k->store(per_sm, std::memory_order_relaxed);
     }
     return (int)std::min<long long>(blocks, (long long)per_sm * tc::sm_count());
 }
 
-template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD>
+template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD, bool RES>
 ret_status launch_ln_forward(const T* x, const T* res, const W* w, const W* b, T* y, T* sum_out, float* mean,
                              float* rstd, long long rows, int D, float eps, cudaStream_t st) {
-    static std::atomic<int> known[33];
+    static StayingBlocks known;
     const int chunks = D / VE;
     const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
     const int threads = WARP ? kLnThreads : lanes;
     const long long per_block = WARP ? threads / lanes : 1;
-    const auto kernel = ln_forward_kernel<T, W, VE, EPT, WARP, HOLD>;
-    const int grid = staying_blocks(kernel, known, threads, 0, (rows + per_block - 1) / per_block);
-    kernel<<<grid, threads, 0, st>>>(x, res, w, b, y, sum_out, mean, rstd, (unsigned)rows, D, eps, lanes);
-    return launch_status();
+    const size_t smem = RowStream<T, VE, EPT, RES ? 2 : 1, 0>::bytes(threads);
+    const auto kernel = ln_forward_kernel<T, W, VE, EPT, WARP, HOLD, RES>;
+    const int grid = staying_blocks(kernel, known, threads, smem, (rows + per_block - 1) / per_block);
+    if (grid == 0) return RET_ERR_CUDA;
+    return tc::launch_dependent(kernel, dim3(grid), threads, smem, st, x, res, w, b, y, sum_out, mean, rstd,
+                                (unsigned)rows, D, eps, lanes) == cudaSuccess
+               ? RET_OK
+               : RET_ERR_CUDA;
 }
 
-template <typename T, typename W, int VE>
+template <typename T, typename W, int VE, bool RES>
 ret_status launch_ln_forward_width(const T* x, const T* res, const W* w, const W* b, T* y, T* sum_out, float* mean,
                                    float* rstd, long long rows, int D, float eps, cudaStream_t st) {
 #define RET_LN_FORWARD(LANES, EPT, WARP, HOLD) \
     if (D <= LANES * EPT)                      \
-    return launch_ln_forward<T, W, VE, EPT, WARP, HOLD>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st)
+    return launch_ln_forward<T, W, VE, EPT, WARP, HOLD, RES>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st)
     RET_LN_FORWARD(32, 8, true, true);
     RET_LN_FORWARD(32, 16, true, true);
     RET_LN_FORWARD(512, 16, false, true);
+    if constexpr (RowStream<T, VE, 32, RES ? 2 : 1, 0>::bytes(512) <= kLnMaxShared) RET_LN_FORWARD(512, 32, false, false);
+    return RET_ERR_UNSUPPORTED;  // not reached: wider rows are not sent here
 #undef RET_LN_FORWARD
-    return launch_ln_forward<T, W, VE, 32, false, false>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
 }
 
-// Rows in registers up to 16,384 elements, in 16-byte vectors where every row starts on 16 bytes,
-// else element by element; longer rows (and 2^30 rows and more) in three passes.
+// Rows of up to 8,192 elements (16,384 where two of them fit shared memory) are read once, in
+// 16-byte vectors where every row starts on 16 bytes, else element by element; longer rows (and
+// 2^30 rows and more) in three passes.
 template <typename T, typename W>
 ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, const void* b_, void* y_,
                              void* sum_out_, float* mean, float* rstd, long long rows, int D, float eps,
@@ -664,53 +675,75 @@ ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, c
     const T *x = static_cast<const T*>(x_), *res = static_cast<const T*>(res_);
     const W *w = static_cast<const W*>(w_), *b = static_cast<const W*>(b_);
     T *y = static_cast<T*>(y_), *sum_out = static_cast<T*>(sum_out_);
-    if (D <= 512 * 32 && rows < (1LL << 30)) {
-        if (D % kE == 0 && aligned16(x) && aligned16(res) && aligned16(w) && aligned16(b) && aligned16(y) &&
-            aligned16(sum_out))
-            return launch_ln_forward_width<T, W, kE>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
-        return launch_ln_forward_width<T, W, 1>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
+    constexpr bool kWideSum = RowStream<T, kE, 32, 2, 0>::bytes(512) <= kLnMaxShared;
+    if (D <= (res == nullptr || kWideSum ? 512 * 32 : 512 * 16) && rows < (1LL << 30)) {
+        const bool vec = D % kE == 0 && aligned16(x) && aligned16(res) && aligned16(w) && aligned16(b) &&
+                         aligned16(y) && aligned16(sum_out);
+        auto go = [&](auto kernels) { return kernels(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st); };
+        if (vec) return res ? go(launch_ln_forward_width<T, W, kE, true>) : go(launch_ln_forward_width<T, W, kE, false>);
+        return res ? go(launch_ln_forward_width<T, W, 1, true>) : go(launch_ln_forward_width<T, W, 1, false>);
     }
     ln_forward_rows_kernel<T, W><<<block_rows(rows), kLnThreads, 0, st>>>(x, res, w, b, y, sum_out, mean, rstd,
                                                                           (size_t)rows, D, eps);
     return launch_status();
 }
 
-template <typename T, typename W, int VE, int EPT, bool WARP>
+template <typename W>
+ret_status launch_ln_reduce(const float* part, int parts, W* dw, W* db, int D, cudaStream_t st) {
+    const unsigned blocks = (unsigned)((2LL * ln_pitch(D) + kReduceColumns - 1) / kReduceColumns);
+    return tc::launch_dependent(ln_reduce_kernel<W>, dim3(blocks), kLnThreads, 0, st, part, parts, dw, db, D) == cudaSuccess
+               ? RET_OK
+               : RET_ERR_CUDA;
+}
+
+template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM>
 ret_status launch_ln_backward(const T* dy, const T* x, const W* w, const float* mean, const float* rstd, const T* dsum,
                               T* dx, W* dw, W* db, long long rows, int D, cudaStream_t st) {
     const int chunks = D / VE;
     const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
-    const int threads = WARP ? kLnThreads : lanes;
-    const size_t smem = WARP ? sizeof(float) * 2 * D : 0;
-    const long long per_block = WARP ? threads / lanes : 1;
-    static std::atomic<int> known[33];
-    const auto kernel = ln_backward_kernel<T, W, VE, EPT, WARP>;
-    const int grid = staying_blocks(kernel, known, threads, smem, (rows + per_block - 1) / per_block);
+    // groups of whole warps: as many as there are rows for, up to 512 threads
+    const int groups = WARP ? kLnThreads / lanes : (int)std::max<long long>(1, std::min<long long>(std::min(kLnGroups, 512 / lanes), rows / tc::sm_count()));
+    const int threads = groups * lanes;
+    const size_t ring = RowStream<T, VE, EPT, SUM ? 3 : 2, 2>::bytes(threads);
+    const size_t smem = std::max(ring, sizeof(float) * 2 * ln_pitch(D));
+    static StayingBlocks known;
+    const auto kernel = ln_backward_kernel<T, W, VE, EPT, WARP, SUM>;
+    // A block leaves a row of partial sums, 8 D bytes written and read again: four rows or more
+    // each, unless that would leave SMs idle.
+    const long long most = (rows + groups - 1) / groups;
+    int grid = staying_blocks(kernel, known, threads, smem,
+                              std::max((most + 3) / 4, std::min<long long>(most, tc::sm_count())));
+    if (grid == 0) return RET_ERR_CUDA;
     float* part = nullptr;
     if (dw || db) {
         tc::keep_pool_memory();
-        if (cudaMallocAsync(reinterpret_cast<void**>(&part), sizeof(float) * 2 * (size_t)grid * D, st) != cudaSuccess)
+        if (cudaMallocAsync(reinterpret_cast<void**>(&part), sizeof(float) * 2 * (size_t)grid * ln_pitch(D), st) !=
+            cudaSuccess)
             return RET_ERR_CUDA;
     }
-    kernel<<<grid, threads, smem, st>>>(dy, x, w, mean, rstd, dsum, dx, part, (unsigned)rows, D, lanes);
-    ret_status r = launch_status();
+    ret_status r = tc::launch_dependent(kernel, dim3(grid), threads, smem, st, dy, x, w, mean, rstd, dsum, dx, part,
+                                        (unsigned)rows, D, lanes) == cudaSuccess
+                       ? RET_OK
+                       : RET_ERR_CUDA;
     if (part) {
-        if (r == RET_OK) {
-            ln_reduce_kernel<W><<<(unsigned)((2LL * D + 31) / 32), kLnThreads, 0, st>>>(part, grid, dw, db, D);
-            r = launch_status();
-        }
+        if (r == RET_OK) r = launch_ln_reduce(part, grid, dw, db, D, st);
         if (cudaFreeAsync(part, st) != cudaSuccess && r == RET_OK) r = RET_ERR_CUDA;
     }
     return r;
 }
 
-template <typename T, typename W, int VE>
+template <typename T, typename W, int VE, bool SUM>
 ret_status launch_ln_backward_width(const T* dy, const T* x, const W* w, const float* mean, const float* rstd,
                                     const T* dsum, T* dx, W* dw, W* db, long long rows, int D, cudaStream_t st) {
-    if (D <= 32 * 8) return launch_ln_backward<T, W, VE, 8, true>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
-    if (D <= 32 * 16) return launch_ln_backward<T, W, VE, 16, true>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
-    if (D <= 512 * 8) return launch_ln_backward<T, W, VE, 8, false>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
-    return launch_ln_backward<T, W, VE, 16, false>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
+#define RET_LN_BACKWARD(LANES, EPT, WARP) \
+    if (D <= LANES * EPT)                 \
+    return launch_ln_backward<T, W, VE, EPT, WARP, SUM>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st)
+    RET_LN_BACKWARD(32, 8, true);
+    RET_LN_BACKWARD(32, 16, true);
+    if constexpr (VE == 1) RET_LN_BACKWARD(512, 8, false);
+    RET_LN_BACKWARD(512, 16, false);
+#undef RET_LN_BACKWARD
+    return RET_ERR_UNSUPPORTED;  // not reached: wider rows are not sent here
 }
 
 // Up to 8,192 columns in one pass; wider (and 2^30 rows and more): the column sums and dx in a
@@ -725,9 +758,10 @@ ret_status launch_layer_norm_backward(const void* dy_, const void* x_, const voi
     T* dx = static_cast<T*>(dx_);
     W *dw = static_cast<W*>(dw_), *db = static_cast<W*>(db_);
     if (D <= 8192 && rows < (1LL << 30)) {
-        if (D % kE == 0 && aligned16(dy) && aligned16(x) && aligned16(w) && aligned16(dsum) && aligned16(dx))
-            return launch_ln_backward_width<T, W, kE>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
-        return launch_ln_backward_width<T, W, 1>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
+        const bool vec = D % kE == 0 && aligned16(dy) && aligned16(x) && aligned16(w) && aligned16(dsum) && aligned16(dx);
+        auto go = [&](auto kernels) { return kernels(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st); };
+        if (vec) return dsum ? go(launch_ln_backward_width<T, W, kE, true>) : go(launch_ln_backward_width<T, W, kE, false>);
+        return dsum ? go(launch_ln_backward_width<T, W, 1, true>) : go(launch_ln_backward_width<T, W, 1, false>);
     }
     ret_status r = RET_OK;
     if (dw || db) {
@@ -735,14 +769,13 @@ ret_status launch_layer_norm_backward(const void* dy_, const void* x_, const voi
         const unsigned parts = (unsigned)std::min<long long>(rows, std::max(1u, 8u * tc::sm_count() / cols));
         tc::keep_pool_memory();
         float* part = nullptr;
-        if (cudaMallocAsync(reinterpret_cast<void**>(&part), sizeof(float) * 2 * (size_t)parts * D, st) != cudaSuccess)
+        if (cudaMallocAsync(reinterpret_cast<void**>(&part), sizeof(float) * 2 * (size_t)parts * ln_pitch(D), st) != cudaSuccess)
             return RET_ERR_CUDA;
         ln_backward_columns_kernel<T><<<dim3(cols, parts), kLnThreads, 0, st>>>(dy, x, mean, rstd, part, (size_t)rows,
                                                                                D);
         r = launch_status();
         if (r == RET_OK) {
-            ln_reduce_kernel<W><<<(unsigned)((2LL * D + 31) / 32), kLnThreads, 0, st>>>(part, (int)parts, dw, db, D);
-            r = launch_status();
+            r = launch_ln_reduce(part, (int)parts, dw, db, D, st);
         }
         if (cudaFreeAsync(part, st) != cudaSuccess && r == RET_OK) r = RET_ERR_CUDA;
         if (r != RET_OK) return r;
