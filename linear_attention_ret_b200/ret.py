@@ -12,7 +12,6 @@ state [B, H, dk, dv] fp32. q, k, v share one dtype (float32 or bfloat16).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -156,7 +155,7 @@ def _expect(name, t, shape, dtype=None):
     pointer reaches the library: a wrong size there would read past an allocation."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -384,18 +383,27 @@ def msr_norm_gate(o, gate, eps: float = 1e-5, y=None, stream=None):
     return y
 
 
-@contextlib.contextmanager
-def _launching(device, stream):
-    """The tensors' device is current inside and `stream` (None: that device's current stream) is
-    the one that outputs are allocated and the call is enqueued on; yields its handle."""
+# The calls below are made once per layer and token, so their host time counts: tensors are read
+# once, addresses go to ctypes as integers, and a device or stream is entered only when it is not
+# the current one.
+
+def _elsewhere(device, stream):
+    """None when a call may go straight to the current stream of the current device; else the context in
+    which it may (stream given, or the tensors' device not current). Outputs are allocated there too."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, tensors are on {device}")
-        with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            yield ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _current_stream(device) -> int:
+    # the handle alone: torch.cuda.current_stream builds a Stream object around it (2 us)
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def msr_norm_gate_backward(dy, o, gate, eps: float = 1e-5, dout=None, dgate=None, stream=None):
@@ -408,36 +416,47 @@ def msr_norm_gate_backward(dy, o, gate, eps: float = 1e-5, dout=None, dgate=None
         _expect(name, t, shape, o.dtype)
     dt = _dt(o)
     _cuda(o, gate, dy, dout, dgate)
-    with _launching(o.device, stream) as s:
-        dout = torch.empty_like(o) if dout is None else dout
-        dgate = torch.empty_like(gate) if dgate is None else dgate
-        _check("ret_msr_norm_gate_backward",
-               load().ret_msr_norm_gate_backward(_ptr(dy), _ptr(o), _ptr(gate), _ptr(dout), _ptr(dgate), B, H, N, dv,
-                                                 float(eps), dt, s))
+    away = _elsewhere(o.device, stream)
+    if away is not None:
+        with away:
+            return msr_norm_gate_backward(dy, o, gate, eps, dout, dgate)
+    dout = torch.empty_like(o) if dout is None else dout
+    dgate = torch.empty_like(gate) if dgate is None else dgate
+    _check("ret_msr_norm_gate_backward",
+           load().ret_msr_norm_gate_backward(dy.data_ptr(), o.data_ptr(), gate.data_ptr(), dout.data_ptr(),
+                                             dgate.data_ptr(), B, H, N, dv, eps, dt, _current_stream(o.device)))
     return dout, dgate
 
 
 ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}  # ret_rotary_layout in include/ret.h
+_Strides = _ll * 12  # batch, token and head strides of q, k, q_out and k_out
+
+
+def _view(name, t, shape, dtype):
+    """Checks one tensor of a rotary call; returns its strides."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    strides = t.stride()
+    if strides[3] != 1 and shape[3] > 1:
+        raise ValueError(f"the head dimension of {name} must be contiguous")
+    return strides
 
 
 def _rotate(q, k, q_out, k_out, freqs, positions, starts, offset, layout, inverse, amplitude, q_scale, k_scale,
             stream):
     """One ret_rotary call. Token-major [B, N, H, d] in and head-major [B, H, N, d] out, or with
     inverse the other way round. Outputs that are None are allocated contiguous."""
-    for name, t in (("q", q), ("k", k), ("the output of q", q_out), ("the output of k", k_out)):
-        if t is not None:
-            _rank(name, t, 4)
-
-    def token_major(t, given):
-        return t.transpose(1, 2) if t is not None and given == inverse else t
-
-    B, N, Hq, d = token_major(q, True).shape
-    Hk = 0 if k is None else token_major(k, True).shape[2]
-    if k is None and k_out is not None:
+    _rank("q", q, 4)
+    B, N, Hq, d = q.shape if not inverse else (q.shape[0], q.shape[2], q.shape[1], q.shape[3])
+    device, dtype = q.device, q.dtype
+    Hk = 0
+    if k is not None:
+        _rank("k", k, 4)
+        Hk = k.shape[1 if inverse else 2]
+    elif k_out is not None:
         raise ValueError("an output for k was given without k")
-    _expect("k", k, (B, Hk, N, d) if inverse else (B, N, Hk, d), q.dtype)
-    _expect("the output of q", q_out, (B, N, Hq, d) if inverse else (B, Hq, N, d), q.dtype)
-    _expect("the output of k", k_out, (B, N, Hk, d) if inverse else (B, Hk, N, d), q.dtype)
     rot = 0
     if freqs is not None:
         _rank("freqs", freqs, 1)
@@ -447,31 +466,47 @@ def _rotate(q, k, q_out, k_out, freqs, positions, starts, offset, layout, invers
             raise ValueError(f"freqs rotates {rot} elements of a head of {d}")
     if positions is not None and starts is not None:
         raise ValueError("give positions or starts, not both")
-    _expect("positions", positions, (B, N), torch.int64)
-    _expect("starts", starts, (B,), torch.int64)
+    if positions is not None:
+        _expect("positions", positions, (B, N), torch.int64)
+    if starts is not None:
+        _expect("starts", starts, (B,), torch.int64)
     if layout not in ROTARY_LAYOUTS:
         raise ValueError(f"layout must be one of {tuple(ROTARY_LAYOUTS)}, got {layout!r}")
     dt = _dt(q)
-    for name, t in (("q", q), ("k", k), ("the output of q", q_out), ("the output of k", k_out)):
-        if t is not None and d > 1 and t.stride(3) != 1:
-            raise ValueError(f"the head dimension of {name} must be contiguous")
-    _cuda(freqs, positions, starts)
-    for t in (q, k, q_out, k_out, freqs, positions, starts):
-        if t is not None and (not t.is_cuda or t.device != q.device):
-            raise ValueError(f"tensors must be CUDA tensors on one device, got {q.device} and {t.device}")
-    with _launching(q.device, stream) as s:
-        def out(t, heads):
-            if t is not None:
-                return t
-            return torch.empty((B, N, heads, d) if inverse else (B, heads, N, d), dtype=q.dtype, device=q.device)
-
-        q_out, k_out = out(q_out, Hq), None if k is None else out(k_out, Hk)
-        views = [token_major(t, given) for t, given in ((q, True), (k, True), (q_out, False), (k_out, False))]
-        strides = [None if t is None else (_ll * 3)(*t.stride()[:3]) for t in views]
-        _check("ret_rotary",
-               load().ret_rotary(*(_ptr(t) for t in views), *strides, _ptr(freqs), _ptr(positions), _ptr(starts),
-                                 int(offset), B, N, Hq, Hk, d, rot, ROTARY_LAYOUTS[layout], int(inverse),
-                                 float(amplitude), float(q_scale), float(k_scale), dt, s))
+    heads_first, heads_last = (B, Hq, N, d), (B, N, Hq, d)
+    shapes = [heads_first, (B, Hk, N, d), heads_last, (B, N, Hk, d)]
+    if not inverse:
+        shapes = shapes[2:] + shapes[:2]
+    sq = _view("q", q, shapes[0], dtype)
+    sk = None if k is None else _view("k", k, shapes[1], dtype)
+    sqo = None if q_out is None else _view("the output of q", q_out, shapes[2], dtype)
+    sko = None if k_out is None else _view("the output of k", k_out, shapes[3], dtype)
+    for t in (q, k, q_out, k_out):
+        if t is not None and (t.device != device or not t.is_cuda):
+            raise ValueError(f"tensors must be CUDA tensors on one device, got {device} and {t.device}")
+    for t in (freqs, positions, starts):
+        if t is not None and (t.device != device or not t.is_contiguous()):
+            raise ValueError(f"tables must be contiguous and on {device}, got {t.device}")
+    away = _elsewhere(device, stream)
+    if away is not None:
+        with away:
+            return _rotate(q, k, q_out, k_out, freqs, positions, starts, offset, layout, inverse, amplitude, q_scale,
+                           k_scale, None)
+    if q_out is None:
+        q_out = q.new_empty(shapes[2])
+        sqo = q_out.stride()
+    if k is None:
+        sk = sko = (0, 0, 0, 0)
+    elif k_out is None:
+        k_out = k.new_empty(shapes[3])
+        sko = k_out.stride()
+    n, h = (2, 1) if inverse else (1, 2)  # token and head dimension of the inputs; the outputs' are the other way round
+    strides = _Strides(sq[0], sq[n], sq[h], sk[0], sk[n], sk[h], sqo[0], sqo[h], sqo[n], sko[0], sko[h], sko[n])
+    at = ctypes.addressof(strides)
+    _check("ret_rotary",
+           load().ret_rotary(q.data_ptr(), _address(k), q_out.data_ptr(), _address(k_out), at, at + 24, at + 48, at + 72,
+                             _address(freqs), _address(positions), _address(starts), offset, B, N, Hq, Hk, d, rot,
+                             ROTARY_LAYOUTS[layout], inverse, amplitude, q_scale, k_scale, dt, _current_stream(device)))
     return q_out, k_out
 
 
@@ -503,19 +538,23 @@ def rotary_backward(dq, dk, freqs, positions=None, starts=None, offset=0, layout
 
 def _norm_args(x, weight, bias):
     """x [..., D]; weight and bias [D] of x's dtype or fp32, each or both None. Returns (rows, D, weight dtype)."""
-    if x.dim() == 0:
+    shape = x.shape
+    if not shape:
         raise ValueError("x must have at least one dimension")
-    D = x.shape[-1]
+    D = shape[-1]
     if D == 0:
-        raise ValueError(f"x must have rows of at least one element, got shape {tuple(x.shape)}")
+        raise ValueError(f"x must have rows of at least one element, got shape {tuple(shape)}")
     _expect("weight", weight, (D,))
     _expect("bias", bias, (D,))
     w = weight if weight is not None else bias
-    if w is not None and w.dtype not in (x.dtype, torch.float32):
-        raise ValueError(f"weight and bias must be {x.dtype} or torch.float32, got {w.dtype}")
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise ValueError(f"weight and bias must share one dtype, got {weight.dtype} and {bias.dtype}")
-    return x.numel() // D, D, x.dtype if w is None else w.dtype
+    if w is None:
+        return x.numel() // D, D, x.dtype
+    wdtype = w.dtype
+    if wdtype != torch.float32 and wdtype != x.dtype:
+        raise ValueError(f"weight and bias must be {x.dtype} or torch.float32, got {wdtype}")
+    if weight is not None and bias is not None and wdtype != bias.dtype:
+        raise ValueError(f"weight and bias must share one dtype, got {wdtype} and {bias.dtype}")
+    return x.numel() // D, D, wdtype
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, y=None, sum_out=None, mean=None,
@@ -525,22 +564,32 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, y=No
     (y, sum_out). mean and rstd (fp32, x's shape without D) receive the row statistics for
     layer_norm_backward if given. y and sum_out may each be the x or the residual tensor."""
     rows, D, wdtype = _norm_args(x, weight, bias)
-    for name, t in (("residual", residual), ("y", y), ("sum_out", sum_out)):
-        _expect(name, t, x.shape, x.dtype)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _expect(name, t, x.shape[:-1], torch.float32)
+    if residual is not None:
+        _expect("residual", residual, x.shape, x.dtype)
+    if y is not None:
+        _expect("y", y, x.shape, x.dtype)
+    if sum_out is not None:
+        _expect("sum_out", sum_out, x.shape, x.dtype)
+    if mean is not None:
+        _expect("mean", mean, x.shape[:-1], torch.float32)
+    if rstd is not None:
+        _expect("rstd", rstd, x.shape[:-1], torch.float32)
     if sum_out is not None and residual is None:
         raise ValueError("sum_out was given without a residual")
     dt = _dt(x)
     _cuda(x, weight, bias, residual, y, sum_out, mean, rstd)
-    with _launching(x.device, stream) as s:
-        y = torch.empty_like(x) if y is None else y
-        if residual is not None and sum_out is None:
-            sum_out = torch.empty_like(x)
-        _check("ret_layer_norm",
-               load().ret_layer_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(y), _ptr(sum_out),
-                                     _ptr(mean), _ptr(rstd), rows, D, float(eps), dt,
-                                     RET_BF16 if wdtype == torch.bfloat16 else RET_F32, s))
+    away = _elsewhere(x.device, stream)
+    if away is not None:
+        with away:
+            return layer_norm(x, weight, bias, eps, residual, y, sum_out, mean, rstd)
+    if y is None:
+        y = torch.empty_like(x)
+    if residual is not None and sum_out is None:
+        sum_out = torch.empty_like(x)
+    _check("ret_layer_norm",
+           load().ret_layer_norm(x.data_ptr(), _address(residual), _address(weight), _address(bias), y.data_ptr(),
+                                 _address(sum_out), _address(mean), _address(rstd), rows, D, eps, dt,
+                                 RET_BF16 if wdtype == torch.bfloat16 else RET_F32, _current_stream(x.device)))
     return y if residual is None else (y, sum_out)
 
 
@@ -562,14 +611,19 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dsum=None, dweight=True, dbia
         _expect(name, t, x.shape[:-1], torch.float32)
     dt = _dt(x)
     _cuda(dy, x, weight, mean, rstd, dsum, dx)
-    with _launching(x.device, stream) as s:
-        dx = torch.empty_like(x) if dx is None else dx
-        dw = torch.empty(D, dtype=wd, device=x.device) if dweight and weight is not None else None
-        db = torch.empty(D, dtype=wd, device=x.device) if dbias else None
-        _check("ret_layer_norm_backward",
-               load().ret_layer_norm_backward(_ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dsum),
-                                              _ptr(dx), _ptr(dw), _ptr(db), rows, D, dt,
-                                              RET_BF16 if wd == torch.bfloat16 else RET_F32, s))
+    away = _elsewhere(x.device, stream)
+    if away is not None:
+        with away:
+            return layer_norm_backward(dy, x, weight, mean, rstd, dsum, dweight, dbias, wdtype, dx)
+    if dx is None:
+        dx = torch.empty_like(x)
+    dw = torch.empty_like(weight) if dweight and weight is not None else None
+    db = x.new_empty(D, dtype=wd) if dbias else None
+    _check("ret_layer_norm_backward",
+           load().ret_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _address(weight), mean.data_ptr(),
+                                          rstd.data_ptr(), _address(dsum), dx.data_ptr(), _address(dw), _address(db),
+                                          rows, D, dt, RET_BF16 if wd == torch.bfloat16 else RET_F32,
+                                          _current_stream(x.device)))
     return dx, dw, db
 
 
