@@ -95,7 +95,14 @@ __device__ __forceinline__ RowThreads row_threads(int lanes) {
     return t;
 }
 
-// A thread's EPT elements of a row: vectors sub, sub + lanes, ... of VE elements.
+// A thread's EPT elements of a row: CH vectors of VE elements, 32 vectors apart, the first of them
+// number row_first. A warp's vectors lie together, so the distances are known when the kernel is
+// compiled (fewer than 32 lanes of a warp hold at most one vector each).
+template <int CH>
+__device__ __forceinline__ int row_first(const RowThreads& t) {
+    return (t.sub >> 5) * 32 * CH + (t.sub & 31);
+}
+
 template <typename T, int VE, int EPT>
 struct RowPart {
     using V = Vec<T, VE>;
@@ -135,7 +142,7 @@ struct RowStream {
     const float* stat[N_STAT > 0 ? N_STAT : 1];
     unsigned next, step, rows;  // the next row to copy
     long long stride;           // elements from a row to the next of this thread
-    int gap;                    // elements from a vector to the next of this thread
+    static constexpr int kGap = 32 * VE;  // elements from a vector to the next of this thread
     bool has[CH];
     unsigned char* slots;          // this thread's place in slot 0
     int put, get;                  // the slot to fill and the slot to read next
@@ -151,8 +158,8 @@ struct RowStream {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     if (!has[c]) continue;
-                    if (kAsync) copy_async<kAsync ? (int)sizeof(Raw) : 4>(slots + (put * N * CH + t * CH + c) * pitch, src[t] + c * gap);
-                    else held[kAsync ? 0 : t][c] = Part::V::load_cs(src[t] + c * gap);
+                    if (kAsync) copy_async<kAsync ? (int)sizeof(Raw) : 4>(slots + (put * N * CH + t * CH + c) * pitch, src[t] + c * kGap);
+                    else held[kAsync ? 0 : t][c] = Part::V::load_cs(src[t] + c * kGap);
                 }
                 src[t] += stride;
             }
@@ -176,10 +183,10 @@ struct RowStream {
         step = step_;
         rows = rows_;
         stride = (long long)step * D;
-        gap = t.lanes * VE;
+        const int first = row_first<CH>(t);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-            src[k] += row < rows ? (size_t)row * D + t.sub * VE : 0;
+            src[k] += row < rows ? (size_t)row * D + first * VE : 0;
         }
         pitch = blockDim.x * (int)sizeof(Raw);
         slots = static_cast<unsigned char*>(smem) + threadIdx.x * sizeof(Raw);
@@ -189,7 +196,7 @@ struct RowStream {
         put = get = 0;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            has[c] = t.sub + c * t.lanes < chunks;
+            has[c] = first + c * 32 < chunks;
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 if (!kAsync) held[kAsync ? 0 : k][c] = Part::V::zero();
@@ -233,19 +240,19 @@ struct RowStream {
         }
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            if (has[c]) Part::V::store(row + c * gap, e + c * VE);
+            if (has[c]) Part::V::store(row + c * kGap, e + c * VE);
         }
     }
 };
 
 // Pairs of a thread's columns of a weight, `none` where there is no weight or no column.
 template <typename W, int VE, int EPT>
-__device__ __forceinline__ void column_weights(const W* w, float none, F2 (&f)[EPT / 2], int sub, int lanes,
+__device__ __forceinline__ void column_weights(const W* w, float none, F2 (&f)[EPT / 2], const RowThreads& t,
                                                int chunks) {
     float e[EPT];
 #pragma unroll
     for (int c = 0; c < EPT / VE; ++c) {
-        const int i = sub + c * lanes;
+        const int i = row_first<EPT / VE>(t) + c * 32;
 #pragma unroll
         for (int k = 0; k < VE; ++k) e[c * VE + k] = none;
         if (w && i < chunks) ln_weights<W, VE>(w + i * VE, e + c * VE);
@@ -277,11 +284,11 @@ ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const 
     in.src[0] = x;
     if (RES) in.src[RES] = res;
     in.start(ln_ring, t, base + mine, step, rows, D);
-    size_t at = (size_t)(base + mine) * D + t.sub * VE;
+    size_t at = (size_t)(base + mine) * D + row_first<EPT / VE>(t) * VE;
     F2 w[EPT / 2], b[EPT / 2];
     if (HOLD) {
-        column_weights<W, VE, EPT>(weight, 1.f, w, t.sub, lanes, D / VE);
-        column_weights<W, VE, EPT>(bias, 0.f, b, t.sub, lanes, D / VE);
+        column_weights<W, VE, EPT>(weight, 1.f, w, t, D / VE);
+        column_weights<W, VE, EPT>(bias, 0.f, b, t, D / VE);
     }
     if (!WARP) __syncthreads();
     for (int flip = 0; base < rows; base += step, at += in.stride, flip ^= 1) {
@@ -312,8 +319,8 @@ ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const 
         if (r < rows) {
             if (RES && sum_out) in.store(sum_out + at, v);
             if (!HOLD) {
-                column_weights<W, VE, EPT>(weight, 1.f, w, t.sub, lanes, D / VE);
-                column_weights<W, VE, EPT>(bias, 0.f, b, t.sub, lanes, D / VE);
+                column_weights<W, VE, EPT>(weight, 1.f, w, t, D / VE);
+                column_weights<W, VE, EPT>(bias, 0.f, b, t, D / VE);
             }
             const F2 scale = F2(rs, rs);
 #pragma unroll
@@ -343,7 +350,6 @@ ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const 
     __shared__ RowShared sm_all[WARP ? 1 : kLnGroups][2];
     const RowThreads t = row_threads(lanes);
     RowShared(&sm)[2] = sm_all[WARP ? 0 : t.group];
-    const int sub = t.sub;
     const unsigned per_block = t.groups, mine = t.group, step = gridDim.x * per_block;
     const float inv = 1.f / (float)D;
     if (!WARP) {
@@ -359,9 +365,9 @@ ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const 
     in.stat[0] = mean;
     in.stat[1] = rstd;
     in.start(ln_ring, t, base + mine, step, rows, D);
-    size_t at = (size_t)(base + mine) * D + sub * VE;
+    size_t at = (size_t)(base + mine) * D + row_first<EPT / VE>(t) * VE;
     F2 w[P], dw[P], db[P];
-    column_weights<W, VE, EPT>(weight, 1.f, w, sub, lanes, D / VE);
+    column_weights<W, VE, EPT>(weight, 1.f, w, t, D / VE);
 #pragma unroll
     for (int i = 0; i < P; ++i) dw[i] = db[i] = F2(0.f, 0.f);
     if (!WARP) t.meet();
@@ -423,7 +429,7 @@ ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const 
             for (int i = 0; i < P; ++i) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int e = 2 * i + k, at_col = (sub + e / VE * lanes) * VE + e % VE;
+                    const int e = 2 * i + k, at_col = (row_first<EPT / VE>(t) + e / VE * 32) * VE + e % VE;
                     if (!in.has[e / VE]) continue;
                     const float a = k ? dw[i].hi() : dw[i].lo(), d = k ? db[i].hi() : db[i].lo();
                     acc[at_col] = q ? acc[at_col] + a : a;

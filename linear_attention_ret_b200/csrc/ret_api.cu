@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -27,6 +28,8 @@ constexpr int kMaxGridY = 65535;
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 inline ret_status launch_status() {
     return cudaGetLastError() == cudaSuccess ? RET_OK : RET_ERR_CUDA;
@@ -606,6 +609,21 @@ inline unsigned block_rows(long long rows) {
     return (unsigned)std::min<long long>(rows, (long long)32 * tc::sm_count());
 }
 
+// Elements of one access: 16 bytes where every row (and weight) starts on 16 bytes, pairs of
+// 2-byte elements where on 4, else single elements.
+inline int norm_vector(size_t elt, size_t welt, int D, std::initializer_list<const void*> rows,
+                       std::initializer_list<const void*> weights) {
+    auto fits = [&](int ve) {
+        if (D % ve != 0) return false;
+        for (const void* p : rows)
+            if (!aligned_to(p, ve * elt)) return false;
+        for (const void* p : weights)
+            if (!aligned_to(p, std::min<size_t>(16, ve * welt))) return false;
+        return true;
+    };
+    const int widest = 16 / (int)elt;
+    return fits(widest) ? widest : elt == 2 && fits(2) ? 2 : 1;
+}
 inline int lanes_for(int chunks) {  // a power of two up to 32
     int n = 1;
     while (n < chunks && n < 32) n *= 2;
@@ -677,10 +695,11 @@ ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, c
     T *y = static_cast<T*>(y_), *sum_out = static_cast<T*>(sum_out_);
     constexpr bool kWideSum = RowStream<T, kE, 32, 2, 0>::bytes(512) <= kLnMaxShared;
     if (D <= (res == nullptr || kWideSum ? 512 * 32 : 512 * 16) && rows < (1LL << 30)) {
-        const bool vec = D % kE == 0 && aligned16(x) && aligned16(res) && aligned16(w) && aligned16(b) &&
-                         aligned16(y) && aligned16(sum_out);
         auto go = [&](auto kernels) { return kernels(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st); };
-        if (vec) return res ? go(launch_ln_forward_width<T, W, kE, true>) : go(launch_ln_forward_width<T, W, kE, false>);
+        const int ve = norm_vector(sizeof(T), sizeof(W), D, {x, res, y, sum_out}, {w, b});
+        if (ve == kE) return res ? go(launch_ln_forward_width<T, W, kE, true>) : go(launch_ln_forward_width<T, W, kE, false>);
+        if constexpr (sizeof(T) == 2)
+            if (ve == 2) return res ? go(launch_ln_forward_width<T, W, 2, true>) : go(launch_ln_forward_width<T, W, 2, false>);
         return res ? go(launch_ln_forward_width<T, W, 1, true>) : go(launch_ln_forward_width<T, W, 1, false>);
     }
     ln_forward_rows_kernel<T, W><<<block_rows(rows), kLnThreads, 0, st>>>(x, res, w, b, y, sum_out, mean, rstd,
@@ -740,7 +759,7 @@ ret_status launch_ln_backward_width(const T* dy, const T* x, const W* w, const f
     return launch_ln_backward<T, W, VE, EPT, WARP, SUM>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st)
     RET_LN_BACKWARD(32, 8, true);
     RET_LN_BACKWARD(32, 16, true);
-    if constexpr (VE == 1) RET_LN_BACKWARD(512, 8, false);
+    if constexpr (VE <= 2) RET_LN_BACKWARD(512, 8, false);
     RET_LN_BACKWARD(512, 16, false);
 #undef RET_LN_BACKWARD
     return RET_ERR_UNSUPPORTED;  // not reached: wider rows are not sent here
@@ -758,9 +777,11 @@ ret_status launch_layer_norm_backward(const void* dy_, const void* x_, const voi
     T* dx = static_cast<T*>(dx_);
     W *dw = static_cast<W*>(dw_), *db = static_cast<W*>(db_);
     if (D <= 8192 && rows < (1LL << 30)) {
-        const bool vec = D % kE == 0 && aligned16(dy) && aligned16(x) && aligned16(w) && aligned16(dsum) && aligned16(dx);
         auto go = [&](auto kernels) { return kernels(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st); };
-        if (vec) return dsum ? go(launch_ln_backward_width<T, W, kE, true>) : go(launch_ln_backward_width<T, W, kE, false>);
+        const int ve = norm_vector(sizeof(T), sizeof(W), D, {dy, x, dsum, dx}, {w});
+        if (ve == kE) return dsum ? go(launch_ln_backward_width<T, W, kE, true>) : go(launch_ln_backward_width<T, W, kE, false>);
+        if constexpr (sizeof(T) == 2)
+            if (ve == 2) return dsum ? go(launch_ln_backward_width<T, W, 2, true>) : go(launch_ln_backward_width<T, W, 2, false>);
         return dsum ? go(launch_ln_backward_width<T, W, 1, true>) : go(launch_ln_backward_width<T, W, 1, false>);
     }
     ret_status r = RET_OK;
@@ -837,7 +858,6 @@ ret_status launch_norm_gate_backward(const void* dy_, const void* o_, const void
 constexpr long long kMaxElements = 1LL << 46;  // of one tensor: more than any device holds, so that byte counts fit
 inline size_t elt_size(ret_dtype dt) { return dt == RET_BF16 ? 2 : 4; }
 inline bool valid_dtype(int dt) { return dt == RET_F32 || dt == RET_BF16; }
-inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 // Whether [a, a + na) and [b, b + nb) share a byte; a null pointer shares none.
 inline bool bytes_overlap(const void* a, size_t na, const void* b, size_t nb) {
