@@ -548,10 +548,11 @@ inline int rotary_units(const RotArgs& a, bool half, int ve) {
 }
 
 template <typename T, int VE, bool HALF>
-ret_status launch_rotary_vec(const RotArgs& a, cudaStream_t st) {
+ret_status launch_rotary_vec(const RotArgs& a, int apart, cudaStream_t st) {
     constexpr int kTableBytes = 32 * 1024;  // most shared memory for cos and sin
     RotPlan pl;
     pl.half_units = HALF ? a.rot / 2 / VE : 0;
+    pl.apart = apart;
     pl.tensors = a.x[1].H > 0 ? 2 : 1;
     const int units = rotary_units(a, HALF, VE), heads = std::max(a.x[0].H, a.x[1].H);
     const int groups = std::max(1, kRotThreads / (units * pl.tensors));  // head groups of a block's q (or k)
@@ -572,8 +573,8 @@ ret_status launch_rotary_vec(const RotArgs& a, cudaStream_t st) {
     return launch_status();
 }
 
-// The widest vectors that every row of every view starts on and that the layout's parts are
-// whole numbers of; elements one by one where that is less than a pair (4 bytes).
+// The widest vectors that every row of every view starts on and that the layout's parts are whole
+// numbers of, else single elements; a thread per pair where a head's units outnumber a block.
 template <typename T, bool HALF>
 ret_status launch_rotary(const RotArgs& a, cudaStream_t st) {
     constexpr int kE = 16 / (int)sizeof(T);
@@ -594,9 +595,11 @@ ret_status launch_rotary(const RotArgs& a, cudaStream_t st) {
         return true;
     };
     const bool small = (long long)a.B * a.N < (1LL << 31);  // tokens are counted in 31 bits
-    if (small && fits(kE)) return launch_rotary_vec<T, kE, HALF>(a, st);
-    if (small && fits(kE / 2)) return launch_rotary_vec<T, kE / 2, HALF>(a, st);
-    if (sizeof(T) == 2 && small && fits(2)) return launch_rotary_vec<T, 2, HALF>(a, st);
+    if (small && fits(kE)) return launch_rotary_vec<T, kE, HALF>(a, a.rot / 2, st);
+    if (small && fits(kE / 2)) return launch_rotary_vec<T, kE / 2, HALF>(a, a.rot / 2, st);
+    if (sizeof(T) == 2 && small && fits(2)) return launch_rotary_vec<T, 2, HALF>(a, a.rot / 2, st);
+    if (small && (a.d + 1) / 2 * (a.x[1].H > 0 ? 2 : 1) <= kRotThreads)
+        return launch_rotary_vec<T, 1, true>(a, HALF ? a.rot / 2 : 1, st);
     const size_t total = (size_t)a.B * a.N * (size_t)(a.x[0].H + a.x[1].H) * (size_t)(a.d - a.rot / 2);
     const unsigned grid = (unsigned)std::min<size_t>((total + kRotThreads - 1) / kRotThreads, (size_t)32 * tc::sm_count());
     rotary_kernel<T, HALF><<<grid, kRotThreads, 0, st>>>(a, total);

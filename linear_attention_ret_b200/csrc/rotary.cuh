@@ -52,19 +52,20 @@ __device__ __forceinline__ void rot_angle(const RotArgs& a, long long p, int i, 
 
 // Vectors of VE elements. A thread owns one unit of every `split`-th head of a token's q or k: a unit is VE consecutive elements (VE / 2 pairs) in the interleaved layout, and in
 // the half layout two vectors: those whose elements pair up, or two neighbours behind the rotated
-// part. Threads of neighbouring units and heads lie side by side, so a warp reads whole stretches of a
+// part. With VE = 1 (odd sizes and alignments) a unit is two elements in either layout. Threads of neighbouring units and heads lie side by side, so a warp reads whole stretches of a
 // token-major row. A block holds `tokens` tokens of `split` head groups of q and of k each.
 // cos and sin of a token are formed once per block, in shared memory, and serve all heads of q
 // and k; a thread's first kRotBatch rows are in flight meanwhile. Index
 // arithmetic is once per thread: with divisions per vector the kernel was bound by instruction
 // issue (1.3B-shaped, 134 MB: 40.6 us, now 23.1 us, 5.8 TB/s; batches of two rows 25.9 us).
-constexpr int kRotBatch = 4;
+constexpr int kRotBatch = 4;  // rows in flight per thread
 
 struct RotPlan {
     FastDiv units, split, N;  // units of a head; head groups of a token's q (or k); tokens of a batch
     int tensors;              // 2: q and k, 1: q alone
     int tokens;               // of a block
-    int half_units;           // half layout: units that are rotated
+    int half_units;           // half layout, or VE = 1: units that are rotated
+    int apart;                // and elements from the first of a pair to the second
     int stride;               // of a token's cos (or sin) in shared memory, in floats
 };
 
@@ -139,8 +140,9 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_vec_kernel(const RotArg
     pl.N.divmod(first + t, b, n);
     const int split = (int)pl.split.d, H = on ? v.H : 0;
     const bool pair = HALF && (int)u < pl.half_units;
-    const int at = HALF && !pair ? a.rot + ((int)u - pl.half_units) * 2 * VE : (int)u * VE;
-    const int second_at = !HALF ? 0 : pair ? half : at + VE < a.d ? VE : 0;
+    // pairs next to each other lie like what is behind the rotated part: VE = 1, interleaved
+    const int at = HALF && (!pair || pl.apart == 1) ? (pair ? 0 : a.rot - 2 * VE * pl.half_units) + (int)u * 2 * VE : (int)u * VE;
+    const int second_at = !HALF ? 0 : pair ? pl.apart : at + VE < a.d ? VE : 0;
     const int live = HALF ? (pair ? P : 0) : min(max(half - (int)u * P, 0), P);
     const T* x = static_cast<const T*>(v.in) + b * v.ib + n * v.in_ + g * v.ih + at;
     T* y = static_cast<T*>(v.out) + b * v.ob + n * v.on + g * v.oh + at;
