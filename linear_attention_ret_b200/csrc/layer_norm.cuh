@@ -10,6 +10,8 @@
 // fp32 sum, not of its rounded copy: one rounding less, at no cost.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 
 namespace ret {
@@ -27,9 +29,11 @@ __device__ __forceinline__ void ln_weights(const W* w, float* f) {
 
 // A row's threads: `lanes` lanes of a warp (WARP; a power of two), or `lanes` / 32 whole warps, up
 // to 16; a block holds `groups` of them, each with a row of its own. row_sum adds a value over a
-// row's threads, row_sums two at once; every thread gets the sums. Whole warps meet at a barrier of their
-// group (number group + 1) and take `sm`, one float per warp and value, zero behind the group's
-// warps and not written again before the group's next barrier.
+// row's threads, row_sums two at once; every thread gets the sums. Whole warps meet at a barrier
+// and take `sm`, one float per warp and value, zero behind the row's warps and not written again
+// before the next barrier. row_sum is for blocks of one group. row_sums' groups meet at barriers of
+// their own (number group + 1); a kernel with numbered barriers holds 16 of an SM's for each block, too
+// many where blocks are small (8192 x 1024 forward: 24.5 us against 13.6 us).
 struct RowThreads {
     int sub, lanes, group, groups;
     __device__ __forceinline__ void meet() const {
@@ -63,9 +67,10 @@ __device__ __forceinline__ float row_sum(float v, const RowThreads& t, RowShared
 }
 
 // Two sums for little more than the shuffles of one: after the first exchange the lower half of
-// a warp carries a and the upper half b.
-template <bool WARP>
-__device__ __forceinline__ void row_sums(float& a, float& b, const RowThreads& t, RowShared& sm) {
+// a warp carries a and the upper half b. PAIR: the row's threads are two blocks of a cluster; each warp's
+// sums go to both blocks' sm, and the cluster's barrier takes the place of the block's.
+template <bool WARP, bool PAIR>
+__device__ __forceinline__ void row_sums(float& a, float& b, const RowThreads& t, RowShared (&sm)[PAIR ? 2 : 1]) {
     if (WARP && t.lanes < 32) {
         a = lanes_sum(a, t.lanes);
         b = lanes_sum(b, t.lanes);
@@ -77,9 +82,22 @@ __device__ __forceinline__ void row_sums(float& a, float& b, const RowThreads& t
     v += __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
     v = lanes_sum<16>(v);
     if (!WARP) {
-        if ((lane & 15) == 0) sm[upper][t.sub >> 5] = v;
-        t.meet();
-        v = lanes_sum<kLnWarps>(sm[upper][lane & (kLnWarps - 1)]);
+        const int warp = t.sub >> 5, place = lane & (kLnWarps - 1);
+        if (PAIR) {
+            const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+            if ((lane & 15) == 0) {
+                float* mine = &sm[cluster.block_rank()][upper][warp];
+                *mine = v;
+                *cluster.map_shared_rank(mine, cluster.block_rank() ^ 1) = v;
+            }
+            cluster.sync();
+            v = sm[0][upper][place] + sm[PAIR][upper][place];
+        } else {
+            if ((lane & 15) == 0) sm[0][upper][warp] = v;
+            t.meet();
+            v = sm[0][upper][place];
+        }
+        v = lanes_sum<kLnWarps>(v);
     }
     const float other = __shfl_xor_sync(0xffffffffu, v, 16);
     a = upper ? other : v;
@@ -175,10 +193,11 @@ struct RowStream {
         for (int k = 0; k < N_STAT; ++k) s[k] = next_stat < rows ? __ldg(stat[k] + next_stat) : 0.f;
         next_stat += step;
     }
-    // src and stat are set; issues the first kAhead rows
+    // src and stat are set; issues the first kAhead rows. The stream is of the first `width` of
+    // rows of D elements.
     __device__ __forceinline__ void start(void* smem, const RowThreads& t, unsigned row, unsigned step_, unsigned rows_,
-                                          int D) {
-        const int chunks = D / VE;
+                                          int D, int width) {
+        const int chunks = width / VE;
         next = row;
         step = step_;
         rows = rows_;
@@ -283,7 +302,7 @@ ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const 
     RowStream<T, VE, EPT, RES ? 2 : 1, 0> in;
     in.src[0] = x;
     if (RES) in.src[RES] = res;
-    in.start(ln_ring, t, base + mine, step, rows, D);
+    in.start(ln_ring, t, base + mine, step, rows, D, D);
     size_t at = (size_t)(base + mine) * D + row_first<EPT / VE>(t) * VE;
     F2 w[EPT / 2], b[EPT / 2];
     if (HOLD) {
@@ -340,37 +359,46 @@ ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const 
 // [gridDim.x, 2, ln_pitch(D)]; ln_reduce_kernel adds those in order.
 __host__ __device__ constexpr int ln_pitch(int D) { return (D + 3) / 4 * 4; }
 
-template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM>
+//
+// PAIR: rows too wide for the registers of one block's 512 threads are split over the two blocks
+// of a cluster, each with its columns. Two blocks of 512 threads hold 16,384 columns; a second pass over the
+// rows for the column sums took 95 us at 1024 x 16384 in bf16 (100 MB).
+template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM, bool PAIR>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
 ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const float* __restrict__ mean,
                    const float* __restrict__ rstd, const T* dsum, T* dx, float* __restrict__ part, unsigned rows, int D,
                    int lanes) {
     constexpr int P = EPT / 2;
     extern __shared__ uint4 ln_ring[];  // rows in flight, and at the end column sums
-    __shared__ RowShared sm_all[WARP ? 1 : kLnGroups][2];
+    __shared__ RowShared sm_all[WARP || PAIR ? 1 : kLnGroups][2][PAIR ? 2 : 1];
     const RowThreads t = row_threads(lanes);
-    RowShared(&sm)[2] = sm_all[WARP ? 0 : t.group];
-    const unsigned per_block = t.groups, mine = t.group, step = gridDim.x * per_block;
+    RowShared(&sm)[2][PAIR ? 2 : 1] = sm_all[WARP || PAIR ? 0 : t.group];
+    const unsigned blocks = PAIR ? gridDim.x / 2 : gridDim.x, block = PAIR ? blockIdx.x / 2 : blockIdx.x;
+    const unsigned per_block = t.groups, mine = t.group, step = blocks * per_block;
     const float inv = 1.f / (float)D;
+    // this block's columns
+    const int half = (D / VE + 1) / 2 * VE, left = PAIR ? (int)(blockIdx.x & 1) * half : 0;
+    const int width = !PAIR ? D : left ? D - half : half;
     if (!WARP) {
-        for (int i = t.sub; i < 2 * 2 * kLnWarps; i += lanes) (&sm[0][0][0])[i] = 0.f;
+        for (int i = t.sub; i < (PAIR ? 4 : 2) * 2 * kLnWarps; i += lanes) (&sm[0][0][0][0])[i] = 0.f;
     }
     allow_next_kernel();
     wait_previous_kernel();
-    unsigned base = blockIdx.x * per_block;  // every group of a block makes the same trips
+    unsigned base = block * per_block;  // every group of a block makes the same trips
     RowStream<T, VE, EPT, SUM ? 3 : 2, 2> in;
-    in.src[0] = dy;
-    in.src[1] = x;
-    if (SUM) in.src[SUM ? 2 : 0] = dsum;
+    in.src[0] = dy + left;
+    in.src[1] = x + left;
+    if (SUM) in.src[SUM ? 2 : 0] = dsum + left;
     in.stat[0] = mean;
     in.stat[1] = rstd;
-    in.start(ln_ring, t, base + mine, step, rows, D);
-    size_t at = (size_t)(base + mine) * D + row_first<EPT / VE>(t) * VE;
+    in.start(ln_ring, t, base + mine, step, rows, D, width);
+    size_t at = (size_t)(base + mine) * D + left + row_first<EPT / VE>(t) * VE;
     F2 w[P], dw[P], db[P];
-    column_weights<W, VE, EPT>(weight, 1.f, w, t, D / VE);
+    column_weights<W, VE, EPT>(weight ? weight + left : weight, 1.f, w, t, width / VE);
 #pragma unroll
     for (int i = 0; i < P; ++i) dw[i] = db[i] = F2(0.f, 0.f);
-    if (!WARP) t.meet();
+    if (PAIR) cooperative_groups::this_cluster().sync();
+    else if (!WARP) __syncthreads();
     for (int flip = 0; base < rows; base += step, at += in.stride, flip ^= 1) {
         const unsigned r = base + mine;
         F2 f[SUM ? 3 : 2][P];
@@ -393,7 +421,7 @@ ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const 
             }
         }
         float a = s0.sum(), c = s1.sum();
-        row_sums<WARP>(a, c, t, sm[flip]);
+        row_sums<WARP, PAIR>(a, c, t, sm[flip]);
         if (r < rows) {
             const float m0 = -scale * (a * inv), m1 = -scale * (c * inv);
 #pragma unroll
@@ -404,6 +432,7 @@ ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const 
             in.store(dx + at, u);
         }
     }
+    if (PAIR) cooperative_groups::this_cluster().sync();  // the other block may still write its sums here
     if (!part) return;
     // column sums to shared memory, [2, Dp]: the groups of a warp (WARP) joined first, then one warp or
     // group after another
@@ -439,8 +468,16 @@ ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const 
         }
         __syncthreads();
     }
-    float4* out = reinterpret_cast<float4*>(part + (size_t)blockIdx.x * 2 * Dp);
-    for (int q = threadIdx.x; q < Dp / 2; q += blockDim.x) out[q] = reinterpret_cast<const float4*>(acc)[q];
+    float* out = part + (size_t)block * 2 * Dp + left;
+    if (PAIR) {
+        for (int q = threadIdx.x; q < width; q += blockDim.x) {
+            out[q] = acc[q];
+            out[Dp + q] = acc[Dp + q];
+        }
+    } else {
+        for (int q = threadIdx.x; q < Dp / 2; q += blockDim.x)
+            reinterpret_cast<float4*>(out)[q] = reinterpret_cast<const float4*>(acc)[q];
+    }
 }
 
 // Sum over the block, in every thread. `sm` holds one float per warp and may be reused at once.

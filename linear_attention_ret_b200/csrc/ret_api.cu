@@ -710,6 +710,26 @@ ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, c
     return launch_status();
 }
 
+// A programmatic dependent launch in clusters of `cluster` blocks.
+template <typename... P, typename... A>
+cudaError_t launch_clusters(void (*kernel)(P...), int grid, int cluster, int threads, size_t smem, cudaStream_t st,
+                            A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
 template <typename W>
 ret_status launch_ln_reduce(const float* part, int parts, W* dw, W* db, int D, cudaStream_t st) {
     const unsigned blocks = (unsigned)((2LL * ln_pitch(D) + kReduceColumns - 1) / kReduceColumns);
@@ -718,24 +738,25 @@ ret_status launch_ln_reduce(const float* part, int parts, W* dw, W* db, int D, c
                : RET_ERR_CUDA;
 }
 
-template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM>
+template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM, bool PAIR>
 ret_status launch_ln_backward(const T* dy, const T* x, const W* w, const float* mean, const float* rstd, const T* dsum,
                               T* dx, W* dw, W* db, long long rows, int D, cudaStream_t st) {
-    const int chunks = D / VE;
+    const int chunks = PAIR ? (D / VE + 1) / 2 : D / VE;  // of a block
     const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
     // groups of whole warps: as many as there are rows for, up to 512 threads
-    const int groups = WARP ? kLnThreads / lanes : (int)std::max<long long>(1, std::min<long long>(std::min(kLnGroups, 512 / lanes), rows / tc::sm_count()));
+    const int groups = WARP ? kLnThreads / lanes : PAIR ? 1 : (int)std::max<long long>(1, std::min<long long>(std::min(kLnGroups, 512 / lanes), rows / tc::sm_count()));
     const int threads = groups * lanes;
     const size_t ring = RowStream<T, VE, EPT, SUM ? 3 : 2, 2>::bytes(threads);
     const size_t smem = std::max(ring, sizeof(float) * 2 * ln_pitch(D));
     static StayingBlocks known;
-    const auto kernel = ln_backward_kernel<T, W, VE, EPT, WARP, SUM>;
+    const auto kernel = ln_backward_kernel<T, W, VE, EPT, WARP, SUM, PAIR>;
     // A block leaves a row of partial sums, 8 D bytes written and read again: four rows or more
     // each, unless that would leave SMs idle.
     const long long most = (rows + groups - 1) / groups;
-    int grid = staying_blocks(kernel, known, threads, smem,
-                              std::max((most + 3) / 4, std::min<long long>(most, tc::sm_count())));
+    const long long sets = tc::sm_count() / (PAIR ? 2 : 1);
+    int grid = staying_blocks(kernel, known, threads, smem, std::max((most + 3) / 4, std::min(most, sets)));
     if (grid == 0) return RET_ERR_CUDA;
+    if (PAIR) grid = (int)std::min<long long>(grid, sets);
     float* part = nullptr;
     if (dw || db) {
         tc::keep_pool_memory();
@@ -743,8 +764,8 @@ ret_status launch_ln_backward(const T* dy, const T* x, const W* w, const float* 
             cudaSuccess)
             return RET_ERR_CUDA;
     }
-    ret_status r = tc::launch_dependent(kernel, dim3(grid), threads, smem, st, dy, x, w, mean, rstd, dsum, dx, part,
-                                        (unsigned)rows, D, lanes) == cudaSuccess
+    ret_status r = launch_clusters(kernel, PAIR ? 2 * grid : grid, PAIR ? 2 : 1, threads, smem, st, dy, x, w, mean, rstd,
+                                   dsum, dx, part, (unsigned)rows, D, lanes) == cudaSuccess
                        ? RET_OK
                        : RET_ERR_CUDA;
     if (part) {
@@ -759,16 +780,16 @@ ret_status launch_ln_backward_width(const T* dy, const T* x, const W* w, const f
                                     const T* dsum, T* dx, W* dw, W* db, long long rows, int D, cudaStream_t st) {
 #define RET_LN_BACKWARD(LANES, EPT, WARP) \
     if (D <= LANES * EPT)                 \
-    return launch_ln_backward<T, W, VE, EPT, WARP, SUM>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st)
+    return launch_ln_backward<T, W, VE, EPT, WARP, SUM, false>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st)
     RET_LN_BACKWARD(32, 8, true);
     RET_LN_BACKWARD(32, 16, true);
     if constexpr (VE <= 2) RET_LN_BACKWARD(512, 8, false);
     RET_LN_BACKWARD(512, 16, false);
 #undef RET_LN_BACKWARD
-    return RET_ERR_UNSUPPORTED;  // not reached: wider rows are not sent here
+    return launch_ln_backward<T, W, VE, 16, false, SUM, true>(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
 }
 
-// Up to 8,192 columns in one pass; wider (and 2^30 rows and more): the column sums and dx in a
+// Up to 16,384 columns in one pass; wider (and 2^30 rows and more): the column sums and dx in a
 // pass of their own each.
 template <typename T, typename W>
 ret_status launch_layer_norm_backward(const void* dy_, const void* x_, const void* w_, const float* mean,
@@ -779,7 +800,7 @@ ret_status launch_layer_norm_backward(const void* dy_, const void* x_, const voi
     const W* w = static_cast<const W*>(w_);
     T* dx = static_cast<T*>(dx_);
     W *dw = static_cast<W*>(dw_), *db = static_cast<W*>(db_);
-    if (D <= 8192 && rows < (1LL << 30)) {
+    if (D <= 2 * 512 * 16 && rows < (1LL << 30)) {
         auto go = [&](auto kernels) { return kernels(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st); };
         const int ve = norm_vector(sizeof(T), sizeof(W), D, {dy, x, dsum, dx}, {w});
         if (ve == kE) return dsum ? go(launch_ln_backward_width<T, W, kE, true>) : go(launch_ln_backward_width<T, W, kE, false>);
