@@ -191,6 +191,7 @@ norm_gate_backward_vec_kernel(const T* dy, const T* o, const T* gate, T* dout, T
     const int chunks = dv / VE;
     const float inv_dv = 1.f / (float)dv;
     const unsigned warps = gridDim.x * (kNormThreads / 32);
+    wait_previous_kernel();
     for (unsigned w = blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5); w * kRowsPerWarp < rows; w += warps) {
         const unsigned r = w * kRowsPerWarp + lane / LPR;
         const bool live = r < rows;

@@ -547,8 +547,8 @@ inline int rotary_units(const RotArgs& a, bool half, int ve) {
     return half ? a.rot / 2 / ve + ((a.d - a.rot) / ve + 1) / 2 : a.d / ve;
 }
 
-template <typename T, int VE, bool HALF>
-ret_status launch_rotary_vec(const RotArgs& a, int apart, cudaStream_t st) {
+template <typename T, int VE, bool HALF, int BATCH>
+ret_status launch_rotary_batch(const RotArgs& a, int apart, cudaStream_t st) {
     constexpr int kTableBytes = 32 * 1024;  // most shared memory for cos and sin
     RotPlan pl;
     pl.half_units = HALF ? a.rot / 2 / VE : 0;
@@ -560,7 +560,7 @@ ret_status launch_rotary_vec(const RotArgs& a, int apart, cudaStream_t st) {
     const long long all = (long long)a.B * a.N;
     // head groups of a token: one batch of rows per thread, or as many threads as there are heads
     // where that leaves SMs idle (decode)
-    int split = std::min(groups, (heads + kRotBatch - 1) / kRotBatch);
+    int split = std::min(groups, (heads + BATCH - 1) / BATCH);
     if (all * split < (long long)groups * 2 * tc::sm_count()) split = std::min(groups, heads);
     long long tokens = groups / split;
     if (pl.stride) tokens = std::min<long long>(tokens, std::max(1, kTableBytes / (8 * pl.stride)));
@@ -569,8 +569,17 @@ ret_status launch_rotary_vec(const RotArgs& a, int apart, cudaStream_t st) {
     pl.split = FastDiv((unsigned)split);
     pl.N = FastDiv((unsigned)a.N);
     const size_t smem = (size_t)8 * pl.tokens * pl.stride;
-    rotary_vec_kernel<T, VE, HALF><<<(unsigned)((all + pl.tokens - 1) / pl.tokens), kRotThreads, smem, st>>>(a, pl);
-    return launch_status();
+    return tc::launch_dependent(rotary_vec_kernel<T, VE, HALF, BATCH>, dim3((unsigned)((all + pl.tokens - 1) / pl.tokens)),
+                                kRotThreads, smem, st, a, pl) == cudaSuccess
+               ? RET_OK
+               : RET_ERR_CUDA;
+}
+
+template <typename T, int VE, bool HALF>
+ret_status launch_rotary_vec(const RotArgs& a, int apart, cudaStream_t st) {
+    if constexpr (HALF && VE > 1)
+        if (std::max(a.x[0].H, a.x[1].H) >= 8) return launch_rotary_batch<T, VE, HALF, 8>(a, apart, st);
+    return launch_rotary_batch<T, VE, HALF, 4>(a, apart, st);
 }
 
 // The widest vectors that every row of every view starts on and that the layout's parts are whole
@@ -595,7 +604,8 @@ ret_status launch_rotary(const RotArgs& a, cudaStream_t st) {
         return true;
     };
     const bool small = (long long)a.B * a.N < (1LL << 31);  // tokens are counted in 31 bits
-    if (small && fits(kE)) return launch_rotary_vec<T, kE, HALF>(a, a.rot / 2, st);
+    if constexpr (!(HALF && sizeof(T) == 2))
+        if (small && fits(kE)) return launch_rotary_vec<T, kE, HALF>(a, a.rot / 2, st);
     if (small && fits(kE / 2)) return launch_rotary_vec<T, kE / 2, HALF>(a, a.rot / 2, st);
     if (sizeof(T) == 2 && small && fits(2)) return launch_rotary_vec<T, 2, HALF>(a, a.rot / 2, st);
     if (small && (a.d + 1) / 2 * (a.x[1].H > 0 ? 2 : 1) <= kRotThreads)
@@ -836,9 +846,11 @@ ret_status launch_norm_backward_vec(const T* dy, const T* o, const T* gate, T* d
                                     float eps, size_t rows, cudaStream_t st) {
     const size_t rows_per_block = (size_t)(kNormThreads / 32) * (32 / LPR);
     const size_t blocks = std::min<size_t>((rows + rows_per_block - 1) / rows_per_block, (size_t)32 * tc::sm_count());
-    norm_gate_backward_vec_kernel<T, VE, LPR, CH><<<(unsigned)blocks, kNormThreads, 0, st>>>(
-        dy, o, gate, dout, dgate, FastDiv((unsigned)H), FastDiv((unsigned)N), dv, eps, (unsigned)rows);
-    return launch_status();
+    return tc::launch_dependent(norm_gate_backward_vec_kernel<T, VE, LPR, CH>, dim3((unsigned)blocks), kNormThreads, 0,
+                                st, dy, o, gate, dout, dgate, FastDiv((unsigned)H), FastDiv((unsigned)N), dv, eps,
+                                (unsigned)rows) == cudaSuccess
+               ? RET_OK
+               : RET_ERR_CUDA;
 }
 
 // Rows in registers: whole 16-byte chunks on up to 32 lanes, or single elements on 32 lanes where

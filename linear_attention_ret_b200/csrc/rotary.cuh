@@ -55,10 +55,9 @@ __device__ __forceinline__ void rot_angle(const RotArgs& a, long long p, int i, 
 // part. With VE = 1 (odd sizes and alignments) a unit is two elements in either layout. Threads of neighbouring units and heads lie side by side, so a warp reads whole stretches of a
 // token-major row. A block holds `tokens` tokens of `split` head groups of q and of k each.
 // cos and sin of a token are formed once per block, in shared memory, and serve all heads of q
-// and k; a thread's first kRotBatch rows are in flight meanwhile. Index
+// and k; a thread's first BATCH rows are in flight meanwhile. Index
 // arithmetic is once per thread: with divisions per vector the kernel was bound by instruction
 // issue (1.3B-shaped, 134 MB: 40.6 us, now 23.1 us, 5.8 TB/s; batches of two rows 25.9 us).
-constexpr int kRotBatch = 4;  // rows in flight per thread
 
 struct RotPlan {
     FastDiv units, split, N;  // units of a head; head groups of a token's q (or k); tokens of a batch
@@ -69,17 +68,17 @@ struct RotPlan {
     int stride;               // of a token's cos (or sin) in shared memory, in floats
 };
 
-template <typename T, int VE, bool HALF>
+template <typename T, int VE, bool HALF, int BATCH>
 struct RotUnit {
     using V = Vec<T, VE>;
     static constexpr int P = HALF ? VE : VE / 2;  // frequencies of a unit
-    typename V::Raw lo[kRotBatch], hi[HALF ? kRotBatch : 1];
+    typename V::Raw lo[BATCH], hi[HALF ? BATCH : 1];
 
     // rows h, h + step, ... below H, at x and every `stride` elements; the second vector `second`
     // elements on (half layout, 0: there is none)
     __device__ __forceinline__ void load(const T* x, long long stride, int h, int step, int H, int second) {
 #pragma unroll
-        for (int i = 0; i < kRotBatch; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             if (h + i * step < H) {
                 lo[i] = V::load_cs(x + i * stride);
                 if (HALF && second) hi[HALF ? i : 0] = V::load_cs(x + i * stride + second);
@@ -92,7 +91,7 @@ struct RotUnit {
     __device__ __forceinline__ void turn_store(T* y, long long stride, int h, int step, int H, int second, int live,
                                                const float (&c)[P], const float (&s)[P], float m) {
 #pragma unroll
-        for (int i = 0; i < kRotBatch; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             if (h + i * step >= H) continue;
             float f[VE];
             V::unpack(lo[i], f);
@@ -119,11 +118,13 @@ struct RotUnit {
     }
 };
 
-// Three blocks per SM: the half layout's two vectors per row otherwise take 98 registers and two
-// blocks (gradient at the gated layer's shapes 54.0 us against 50.3 us).
-template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kRotThreads, 3) rotary_vec_kernel(const RotArgs a, const RotPlan pl) {
-    using Unit = RotUnit<T, VE, HALF>;
+// The half layout of bf16 takes vectors of 8 bytes, two per unit: units of 16 bytes need twice the
+// registers and leave three blocks on an SM instead of four (134 MB, 4 heads of 128: 26.9 us against
+// 25.9 us), and with eight heads or more a thread takes eight rows at once (gradient at the gated
+// layer's shapes, 268 MB: 47.0 us with four, 44.6 us with eight, 6.0 TB/s; the interleaved layout gains nothing).
+template <typename T, int VE, bool HALF, int BATCH>
+__global__ void __launch_bounds__(kRotThreads, BATCH > 4 ? 3 : 4) rotary_vec_kernel(const RotArgs a, const RotPlan pl) {
+    using Unit = RotUnit<T, VE, HALF, BATCH>;
     constexpr int P = Unit::P;
     extern __shared__ float4 rot_sm[];
     float* cs = reinterpret_cast<float*>(rot_sm);
@@ -147,6 +148,7 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_vec_kernel(const RotArg
     const T* x = static_cast<const T*>(v.in) + b * v.ib + n * v.in_ + g * v.ih + at;
     T* y = static_cast<T*>(v.out) + b * v.ob + n * v.on + g * v.oh + at;
     const long long si = split * v.ih, so = split * v.oh;
+    wait_previous_kernel();
     Unit r;
     r.load(x, si, (int)g, split, H, second_at);
     for (int j = threadIdx.x; j < tokens * half; j += kRotThreads) {
@@ -165,10 +167,10 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotary_vec_kernel(const RotArg
     }
     for (int h = (int)g;;) {
         r.turn_store(y, so, h, split, H, second_at, live, c, s, m);
-        h += kRotBatch * split;
+        h += BATCH * split;
         if (h >= H) break;
-        x += kRotBatch * si;
-        y += kRotBatch * so;
+        x += BATCH * si;
+        y += BATCH * so;
         r.load(x, si, h, split, H, second_at);
     }
 }
