@@ -315,7 +315,7 @@ typedef enum {
  *                 and scales). The angle is formed in fp64: t keeps its digits at far positions.
  *   p             offset + positions[b, n] if positions ([B, N] int64) is given, else
  *                 offset + n, + starts[b] if starts ([B] int64) is given. Both: rejected.
- * Arithmetic is fp32 (cos and sin within 2^-21), rounded once. An output may be its own input
+ * Arithmetic is fp32 (cos and sin within 2^-21 for angles below 2^28 rad), rounded once. An output may be its own input
  * (same address and strides); an output that is not seen to be disjoint from the other
  * tensors, or that writes an element twice, is rejected with RET_ERR_UNSUPPORTED. Column
  * blocks of one row-strided buffer (same strides, heads at distinct places of a row) count as

@@ -45,10 +45,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr",
-           "-I", os.path.join(ROOT, "include"),
-           os.path.join(CSRC, "ret_api.cu"), "-o", tmp, "-cudart", "static"]
+           "-I", os.path.join(ROOT, "include"), "--threads", "0",
+           *sorted(glob.glob(os.path.join(CSRC, "*.cu"))), "-o", tmp, "-cudart", "static"]
     if verbose:
-        cmd.insert(-5, "-Xptxas=-v")
+        cmd.append("-Xptxas=-v")
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     return LIB

@@ -12,7 +12,7 @@
 
 #include <cooperative_groups.h>
 
-#include "common.cuh"
+#include "vec.cuh"
 
 namespace ret {
 
@@ -137,11 +137,11 @@ struct RowPart {
 };
 
 // The rows that a thread works through: `row`, row + step, ... below `rows`, kAhead of them in
-// flight. Each thread copies its own parts of N tensors' rows (and N_STAT floats per row) into
-// slots of shared memory that no other thread reads, so it waits for its own copies alone, and
-// registers hold no row in flight but its statistics, which are loaded two rows ahead. 2-byte accesses
-// have no asynchronous copy: those wait in registers, one row ahead. Vectors behind the row read as zero; rows behind the last one are
-// not copied, and taking one gives whatever an earlier row left.
+// flight. Each thread copies its own parts of N tensors' rows into slots of shared memory that no
+// other thread reads, so it waits for its own copies alone, and registers hold no row in flight but
+// its N_STAT statistics, loaded two rows ahead. 2-byte accesses have no asynchronous copy: those
+// wait in registers, one row ahead. Vectors behind the row read as zero; rows behind the last one
+// are not copied, and taking one gives whatever an earlier row left.
 template <typename T, int VE, int EPT, int N, int N_STAT>
 struct RowStream {
     using Part = RowPart<T, VE, EPT>;
@@ -152,22 +152,27 @@ struct RowStream {
     static constexpr int kRowBytes = N * CH * (int)sizeof(Raw);
     static constexpr int kSlots = !kAsync ? 0 : kRowBytes <= 64 ? 4 : kRowBytes <= 128 ? 3 : 2;
     static constexpr int kAhead = kAsync ? kSlots - 1 : 1;
-    // [slot][tensor][vector][thread]: neighbouring threads' copies lie side by side (a thread's own slots side by side, threads an odd number
-    // of 16-byte units apart, was a third slower: fp32 8192 x 2048 forward 32.4 us against 24.3 us)
+    // [slot][tensor][vector][thread]: neighbouring threads' copies lie side by side. A thread's own
+    // slots side by side, threads an odd number of 16-byte units apart, met no bank twice either but
+    // was a third slower (fp32 8192 x 2048 forward 32.4 us against 24.3 us).
     static constexpr size_t bytes(int threads) { return (size_t)kSlots * threads * kRowBytes; }
 
     const T* src[N];  // of this thread's first vector of the next row to copy
     const float* stat[N_STAT > 0 ? N_STAT : 1];
-    unsigned next, step, rows;  // the next row to copy
-    long long stride;           // elements from a row to the next of this thread
+    unsigned next, step, rows;            // the next row to copy
+    long long stride;                     // elements from a row to the next of this thread
     static constexpr int kGap = 32 * VE;  // elements from a vector to the next of this thread
     bool has[CH];
-    unsigned char* slots;          // this thread's place in slot 0
-    int put, get;                  // the slot to fill and the slot to read next
-    int pitch;                     // bytes from a vector to the thread's next
+    unsigned char* slots;  // this thread's place in slot 0
+    int put, get;          // the slot to fill and the slot to read next
+    int pitch;             // bytes from a vector to the thread's next
     Raw held[kAsync ? 1 : N][CH];
     float stats[2][N_STAT > 0 ? N_STAT : 1];  // of the current row and the next
     unsigned next_stat;
+
+    __device__ __forceinline__ Raw* at(int slot, int t, int c) const {
+        return reinterpret_cast<Raw*>(slots + (slot * N * CH + t * CH + c) * pitch);
+    }
 
     __device__ __forceinline__ void issue() {
         if (next < rows) {
@@ -176,7 +181,7 @@ struct RowStream {
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     if (!has[c]) continue;
-                    if (kAsync) copy_async<kAsync ? (int)sizeof(Raw) : 4>(slots + (put * N * CH + t * CH + c) * pitch, src[t] + c * kGap);
+                    if (kAsync) copy_async<kAsync ? (int)sizeof(Raw) : 4>(at(put, t, c), src[t] + c * kGap);
                     else held[kAsync ? 0 : t][c] = Part::V::load_cs(src[t] + c * kGap);
                 }
                 src[t] += stride;
@@ -190,7 +195,7 @@ struct RowStream {
     }
     __device__ __forceinline__ void load_stats(float (&s)[N_STAT > 0 ? N_STAT : 1]) {
 #pragma unroll
-        for (int k = 0; k < N_STAT; ++k) s[k] = next_stat < rows ? __ldg(stat[k] + next_stat) : 0.f;
+        for (int k = 0; k < N_STAT; ++k) s[k] = next_stat < rows ? stat[k][next_stat] : 0.f;
         next_stat += step;
     }
     // src and stat are set; issues the first kAhead rows. The stream is of the first `width` of
@@ -220,8 +225,7 @@ struct RowStream {
             for (int k = 0; k < N; ++k) {
                 if (!kAsync) held[kAsync ? 0 : k][c] = Part::V::zero();
                 else if (!has[c])
-                    for (int q = 0; q < kSlots; ++q)
-                        *reinterpret_cast<Raw*>(slots + (q * N * CH + k * CH + c) * pitch) = Part::V::zero();
+                    for (int q = 0; q < kSlots; ++q) *at(q, k, c) = Part::V::zero();
             }
         }
 #pragma unroll
@@ -242,7 +246,7 @@ struct RowStream {
         for (int t = 0; t < N; ++t) {
             Raw q[CH];
 #pragma unroll
-            for (int c = 0; c < CH; ++c) q[c] = kAsync ? *reinterpret_cast<const Raw*>(slots + (get * N * CH + t * CH + c) * pitch) : held[kAsync ? 0 : t][c];
+            for (int c = 0; c < CH; ++c) q[c] = kAsync ? *at(get, t, c) : held[kAsync ? 0 : t][c];
             Part::pairs(q, f[t]);
         }
         if (kAsync) {
@@ -287,8 +291,8 @@ __device__ __forceinline__ void column_weights(const W* w, float none, F2 (&f)[E
 // are read from L1 for every row.
 template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD, bool RES>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
-ln_forward_kernel(const T* x, const T* res, const W* __restrict__ weight, const W* __restrict__ bias, T* y, T* sum_out,
-                  float* __restrict__ mean, float* __restrict__ rstd, unsigned rows, int D, float eps, int lanes) {
+ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y, T* sum_out,
+                  float* mean, float* rstd, unsigned rows, int D, float eps, int lanes) {
     extern __shared__ uint4 ln_ring[];
     __shared__ RowShared sm[2][2];  // one group of whole warps
     const RowThreads t = row_threads(lanes);
@@ -365,8 +369,8 @@ __host__ __device__ constexpr int ln_pitch(int D) { return (D + 3) / 4 * 4; }
 // rows for the column sums took 95 us at 1024 x 16384 in bf16 (100 MB).
 template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM, bool PAIR>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
-ln_backward_kernel(const T* dy, const T* x, const W* __restrict__ weight, const float* __restrict__ mean,
-                   const float* __restrict__ rstd, const T* dsum, T* dx, float* __restrict__ part, unsigned rows, int D,
+ln_backward_kernel(const T* dy, const T* x, const W* weight, const float* mean,
+                   const float* rstd, const T* dsum, T* dx, float* part, unsigned rows, int D,
                    int lanes) {
     constexpr int P = EPT / 2;
     extern __shared__ uint4 ln_ring[];  // rows in flight, and at the end column sums
@@ -573,7 +577,7 @@ ln_backward_columns_kernel(const T* __restrict__ dy, const T* __restrict__ x, co
 constexpr int kReduceColumns = 16, kReduceQuads = kReduceColumns / 4;
 template <typename W>
 __global__ void __launch_bounds__(kLnThreads)
-ln_reduce_kernel(const float* __restrict__ part, int parts, W* __restrict__ dweight, W* __restrict__ dbias, int D) {
+ln_reduce_kernel(const float* part, int parts, W* dweight, W* dbias, int D) {
     __shared__ float4 sm[kLnThreads / 32][kReduceQuads];
     const int Dp = ln_pitch(D), quad = threadIdx.x % kReduceQuads, slice = threadIdx.x / kReduceQuads;
     const int c = blockIdx.x * kReduceColumns + 4 * quad;  // of 2 Dp
@@ -583,7 +587,7 @@ ln_reduce_kernel(const float* __restrict__ part, int parts, W* __restrict__ dwei
     if (c < 2 * Dp) {
 #pragma unroll 4
         for (int p = slice; p < parts; p += kLnThreads / kReduceQuads)
-            add(__ldcg(reinterpret_cast<const float4*>(part + (size_t)p * 2 * Dp + c)));
+            add(*reinterpret_cast<const float4*>(part + (size_t)p * 2 * Dp + c));
     }
 #pragma unroll
     for (int off = kReduceQuads; off < 32; off <<= 1) {

@@ -10,7 +10,7 @@
 // The angle is formed in 64 bits: at p = 2^20 a product in fp32 is off by up to 2^-4 rad.
 #pragma once
 
-#include "common.cuh"
+#include "vec.cuh"
 
 namespace ret {
 
@@ -50,15 +50,16 @@ __device__ __forceinline__ void rot_angle(const RotArgs& a, long long p, int i, 
     s *= a.amplitude * a.sign;
 }
 
-// Vectors of VE elements. A thread owns one unit of every `split`-th head of a token's q or k: a unit is VE consecutive elements (VE / 2 pairs) in the interleaved layout, and in
-// the half layout two vectors: those whose elements pair up, or two neighbours behind the rotated
-// part. With VE = 1 (odd sizes and alignments) a unit is two elements in either layout. Threads of neighbouring units and heads lie side by side, so a warp reads whole stretches of a
-// token-major row. A block holds `tokens` tokens of `split` head groups of q and of k each.
-// cos and sin of a token are formed once per block, in shared memory, and serve all heads of q
-// and k; a thread's first BATCH rows are in flight meanwhile. Index
-// arithmetic is once per thread: with divisions per vector the kernel was bound by instruction
-// issue (1.3B-shaped, 134 MB: 40.6 us, now 23.1 us, 5.8 TB/s; batches of two rows 25.9 us).
-
+// Vectors of VE elements. A thread owns one unit of every `split`-th head of a token's q or k: a
+// unit is VE consecutive elements (VE / 2 pairs) in the interleaved layout, and in the half layout
+// two vectors, those whose elements pair up or two neighbours behind the rotated part. With VE = 1
+// (odd sizes and alignments) a unit is two elements in either layout. Threads of neighbouring
+// units and heads lie side by side, so a warp reads whole stretches of a token-major row. A block
+// holds `tokens` tokens of `split` head groups of q and of k each.
+// cos and sin of a token are formed once per block, in shared memory, and serve all heads of q and
+// k; a thread's first BATCH rows are in flight meanwhile. HBM-bound; index arithmetic is once per
+// thread, as divisions per vector bound the kernel by instruction issue (1.3B-shaped, 134 MB:
+// 40.6 us, now 23.0 us, 5.8 TB/s; batches of two rows 25.9 us).
 struct RotPlan {
     FastDiv units, split, N;  // units of a head; head groups of a token's q (or k); tokens of a batch
     int tensors;              // 2: q and k, 1: q alone
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(kRotThreads, BATCH > 4 ? 3 : 4) rotary_vec_ker
     const int split = (int)pl.split.d, H = on ? v.H : 0;
     const bool pair = HALF && (int)u < pl.half_units;
     // pairs next to each other lie like what is behind the rotated part: VE = 1, interleaved
-    const int at = HALF && (!pair || pl.apart == 1) ? (pair ? 0 : a.rot - 2 * VE * pl.half_units) + (int)u * 2 * VE : (int)u * VE;
+    const int at = !HALF || (pair && pl.apart != 1) ? (int)u * VE
+                                                    : (pair ? 0 : a.rot - 2 * VE * pl.half_units) + (int)u * 2 * VE;
     const int second_at = !HALF ? 0 : pair ? pl.apart : at + VE < a.d ? VE : 0;
     const int live = HALF ? (pair ? P : 0) : min(max(half - (int)u * P, 0), P);
     const T* x = static_cast<const T*>(v.in) + b * v.ib + n * v.in_ + g * v.ih + at;

@@ -500,7 +500,7 @@ def _rotate(q, k, q_out, k_out, freqs, positions, starts, offset, layout, invers
     elif k_out is None:
         k_out = k.new_empty(shapes[3])
         sko = k_out.stride()
-    n, h = (2, 1) if inverse else (1, 2)  # token and head dimension of the inputs; the outputs' are the other way round
+    n, h = (2, 1) if inverse else (1, 2)  # token and head dimension of the inputs; the outputs have them swapped
     strides = _Strides(sq[0], sq[n], sq[h], sk[0], sk[n], sk[h], sqo[0], sqo[h], sqo[n], sko[0], sko[h], sko[n])
     at = ctypes.addressof(strides)
     _check("ret_rotary",
