@@ -46,11 +46,20 @@ inline int sm_count() {
     return n;
 }
 
+// Inside, this thread may make calls that a stream capture forbids: what is set up once per process
+// is also set up when the first call is captured.
+struct RelaxedCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 // Stream-ordered scratch from the device's default pool, which keeps freed memory for the next call.
 inline cudaError_t scratch_alloc(float** p, size_t floats, cudaStream_t st) {
     static std::atomic<bool> done[kMaxDevices];
     const int dev = current_device();
     if (dev >= 0 && dev < kMaxDevices && !done[dev].exchange(true)) {
+        RelaxedCapture relaxed;
         cudaMemPool_t pool;
         uint64_t threshold = UINT64_MAX;
         if (cudaDeviceGetDefaultMemPool(&pool, dev) == cudaSuccess)
@@ -264,6 +273,7 @@ int staying_blocks(Kernel kernel, StayingBlocks& known, int threads, size_t smem
     std::atomic<int>* k = dev >= 0 && dev < kMaxDevices ? &known.per_sm[dev][threads / 32] : nullptr;
     int per_sm = k ? k->load(std::memory_order_relaxed) : 0;
     if (per_sm == 0) {
+        RelaxedCapture relaxed;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kLnMaxShared) != cudaSuccess ||
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
             return 0;

@@ -146,7 +146,7 @@ def test_backward_matches_plain(cuda_lib, rows, D, dtype, wdtype):
     assert all(torch.equal(a, g) for a, g in zip(again, got))  # fixed order: bit for bit
 
 
-@pytest.mark.parametrize("rows,D", [(4000, 64), (3000, 257), (2500, 1024)])
+@pytest.mark.parametrize("rows,D", [(4000, 64), (3000, 257), (2500, 1024), (1500, 770), (700, 9000), (300, 12289)])
 def test_backward_of_many_rows(cuda_lib, rows, D):
     backward_check(cuda_lib, rows, D, bf, f32)
     backward_check(cuda_lib, rows, D, bf, f32, weight=False, residual=True)

@@ -197,7 +197,8 @@ def test_captured_training_step(cuda_lib):
     B, N, H, dk, dv = 1, 128, 2, 64, 128
     freqs = frequencies(dk, schedule="retnet")[0].to(DEV)
     gamma = I.gammas(H).to(DEV)
-    leaves = [randn(B, N, H, d, dtype=bf, seed=i, scale=d ** -0.5).requires_grad_() for i, d in enumerate((dk, dk, dv, dv))]
+    leaves = [randn(B, N, H, d, dtype=bf, seed=i, scale=d ** -0.5).requires_grad_()
+              for i, d in enumerate((dk, dk, dv, dv))]
     lw = randn(dv, seed=7).requires_grad_()
     dy = randn(B, N, H, dv, dtype=bf, seed=8)
 
@@ -233,3 +234,102 @@ def test_on_another_stream(cuda_lib):
     assert torch.cuda.current_stream() == current
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_back_to_back_calls_see_each_others_results(cuda_lib):
+    """Kernels that are placed while the one before drains: a chain in which each call reads what the one
+    before wrote, with and without a synchronise between the calls."""
+    ret = cuda_lib
+    B, N, H, d = 1, 300, 4, 64
+    D = H * d
+    freqs = frequencies(d)[0].to(DEV)
+
+    def chain(sync):
+        def settle():
+            if sync:
+                torch.cuda.synchronize()
+        x, w, b = randn(B, N, D, dtype=bf), randn(D, seed=1), randn(D, seed=2)
+        y, s = torch.empty_like(x), torch.zeros_like(x)
+        mean, rstd = torch.empty(B, N, device=DEV), torch.empty(B, N, device=DEV)
+        q, o = torch.empty(B, H, N, d, dtype=bf, device=DEV), torch.empty(B, N, H, d, dtype=bf, device=DEV)
+        for i in range(40):
+            ret.layer_norm(x, w, b, residual=s, y=y, sum_out=s, mean=mean, rstd=rstd)
+            settle()
+            ret.rotary(y.view(B, N, H, d), None, freqs, offset=i, q_out=q)
+            settle()
+            ret.msr_norm_gate_backward(y.view(B, N, H, d), q, s.view(B, N, H, d), dout=q, dgate=o)
+            settle()
+            _, w, b = ret.layer_norm_backward(o.view(B, N, D), s, w, mean, rstd, dsum=y, dx=x)
+            settle()
+            w, b = w.clamp(-2, 2), b.clamp(-2, 2)
+        torch.cuda.synchronize()
+        return x, s, q, o, w, b
+
+    for got, want in zip(chain(False), chain(True)):
+        assert torch.isfinite(want).all() and torch.equal(got, want)
+
+
+def test_two_threads_at_once(cuda_lib):
+    """Calls from several host threads, each on a stream of its own."""
+    import threading
+    ret = cuda_lib
+    jobs = []
+    for i, (rows, D) in enumerate([(513, 1024), (700, 771), (90, 12000), (4, 16384)]):
+        x, dy, w = randn(rows, D, dtype=bf, seed=i), randn(rows, D, dtype=bf, seed=10 + i), randn(D, seed=20 + i)
+        mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+        ret.layer_norm(x, w, mean=mean, rstd=rstd)
+        jobs.append((dy, x, w, mean, rstd))
+    want = [ret.layer_norm_backward(*j) for j in jobs]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(jobs), []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                for _ in range(30):
+                    got[i] = ret.layer_norm_backward(*jobs[i])
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001 - reported below
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for g, w in zip(got, want):
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+from linear_attention_ret_b200 import ret
+from linear_attention_ret_b200.rotary import frequencies
+x, w = torch.randn(300, 1024, device="cuda").bfloat16(), torch.randn(1024, device="cuda")
+mean, rstd = torch.empty(300, device="cuda"), torch.empty(300, device="cuda")
+q, f = torch.randn(2, 9, 4, 64, device="cuda").bfloat16(), frequencies(64)[0].cuda()
+def calls():
+    y = ret.layer_norm(x, w, mean=mean, rstd=rstd)
+    return [y, *ret.layer_norm_backward(y, x, w, mean, rstd), *ret.rotary(q, q, f),
+            *ret.msr_norm_gate_backward(q, q.view(2, 4, 9, 64), q)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = calls()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, calls()))
+print("same")
+"""
+
+
+def test_first_call_may_be_captured(cuda_lib):
+    """A process whose first calls are made under capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and "same" in p.stdout, p.stderr[-2000:]

@@ -376,3 +376,22 @@ def test_second_backward_raises(plain_library):
     g, = torch.autograd.grad(A.layer_norm(x).square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+# ---------------------------------------------------------------- devices and streams
+
+def test_calls_enter_the_tensors_device_and_the_given_stream(monkeypatch):
+    class Stream:
+        def __init__(self, device):
+            self.device = device
+
+    one, two = torch.device("cuda", 0), torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: ("device", d))
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: ("stream", s))
+    assert ret._elsewhere(one, None) is None
+    assert ret._elsewhere(two, None) == ("device", two)
+    s = Stream(two)
+    assert ret._elsewhere(two, s) == ("stream", s)
+    with pytest.raises(ValueError, match="stream is on"):
+        ret._elsewhere(one, s)
