@@ -384,8 +384,11 @@ def msr_norm_gate(o, gate, eps: float = 1e-5, y=None, stream=None):
 
 
 # The calls below are made once per layer and token, so their host time counts: tensors are read
-# once, addresses go to ctypes as integers, and a device or stream is entered only when it is not
-# the current one.
+# once, addresses go to ctypes as integers, what is absent is not looked at, and a device or stream
+# is entered only when it is not the current one.
+
+_DTYPES = {torch.float32: RET_F32, torch.bfloat16: RET_BF16}
+
 
 def _elsewhere(device, stream):
     """None when a call may go straight to the current stream of the current device; else the context in
@@ -409,104 +412,134 @@ def _address(t):
 def msr_norm_gate_backward(dy, o, gate, eps: float = 1e-5, dout=None, dgate=None, stream=None):
     """Gradients of sum(dy * msr_norm_gate(o, gate, eps)). dy, gate [B, N, H, dv]; o [B, H, N, dv].
     Returns (dout [B, H, N, dv], dgate [B, N, H, dv]); dout may be o, dgate may be gate or dy."""
-    _rank("o", o, 4)
-    B, H, N, dv = o.shape
-    for name, t, shape in (("gate", gate, (B, N, H, dv)), ("dy", dy, (B, N, H, dv)), ("dout", dout, (B, H, N, dv)),
-                           ("dgate", dgate, (B, N, H, dv))):
-        _expect(name, t, shape, o.dtype)
-    dt = _dt(o)
+    shape, dtype, device = o.shape, o.dtype, o.device
+    if len(shape) != 4:
+        _rank("o", o, 4)
+    B, H, N, dv = shape
+    token_major = (B, N, H, dv)
+    _expect("gate", gate, token_major, dtype)
+    _expect("dy", dy, token_major, dtype)
+    if dout is not None:
+        _expect("dout", dout, shape, dtype)
+    if dgate is not None:
+        _expect("dgate", dgate, token_major, dtype)
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _dt(o)
     _cuda(o, gate, dy, dout, dgate)
-    away = _elsewhere(o.device, stream)
+    away = _elsewhere(device, stream)
     if away is not None:
         with away:
             return msr_norm_gate_backward(dy, o, gate, eps, dout, dgate)
-    dout = torch.empty_like(o) if dout is None else dout
-    dgate = torch.empty_like(gate) if dgate is None else dgate
+    if dout is None:
+        dout = torch.empty_like(o)
+    if dgate is None:
+        dgate = torch.empty_like(gate)
     _check("ret_msr_norm_gate_backward",
-           load().ret_msr_norm_gate_backward(dy.data_ptr(), o.data_ptr(), gate.data_ptr(), dout.data_ptr(),
-                                             dgate.data_ptr(), B, H, N, dv, eps, dt, _current_stream(o.device)))
+           (_lib or load()).ret_msr_norm_gate_backward(dy.data_ptr(), o.data_ptr(), gate.data_ptr(), dout.data_ptr(),
+                                                       dgate.data_ptr(), B, H, N, dv, float(eps), dt,
+                                                       _current_stream(device)))
     return dout, dgate
 
 
 ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}  # ret_rotary_layout in include/ret.h
 _Strides = _ll * 12  # batch, token and head strides of q, k, q_out and k_out
+_NO_STRIDES = (0, 0, 0, 0)
 
 
-def _view(name, t, shape, dtype):
-    """Checks one tensor of a rotary call; returns its strides."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+def _view(name, t, shape, dtype, device):
+    """Checks one tensor of a rotary call; returns its strides and whether it is on the device."""
+    if t.shape != shape or t.dtype != dtype:
+        _expect(name, t, shape, dtype)
     strides = t.stride()
     if strides[3] != 1 and shape[3] > 1:
         raise ValueError(f"the head dimension of {name} must be contiguous")
-    return strides
+    return strides, t.device == device
 
 
 def _rotate(q, k, q_out, k_out, freqs, positions, starts, offset, layout, inverse, amplitude, q_scale, k_scale,
             stream):
     """One ret_rotary call. Token-major [B, N, H, d] in and head-major [B, H, N, d] out, or with
     inverse the other way round. Outputs that are None are allocated contiguous."""
-    _rank("q", q, 4)
-    B, N, Hq, d = q.shape if not inverse else (q.shape[0], q.shape[2], q.shape[1], q.shape[3])
-    device, dtype = q.device, q.dtype
-    Hk = 0
+    shape, dtype, device = q.shape, q.dtype, q.device
+    if len(shape) != 4:
+        _rank("q", q, 4)
+    if inverse:
+        B, Hq, N, d = shape
+        q_shape = (B, N, Hq, d)
+    else:
+        B, N, Hq, d = shape
+        q_shape = (B, Hq, N, d)
+    here = q.is_cuda
+    sq = q.stride()
+    if sq[3] != 1 and d > 1:
+        raise ValueError("the head dimension of q must be contiguous")
+    Hk, sk, sko = 0, _NO_STRIDES, _NO_STRIDES
     if k is not None:
-        _rank("k", k, 4)
-        Hk = k.shape[1 if inverse else 2]
+        if k.dim() != 4:
+            _rank("k", k, 4)
+        if inverse:
+            Hk = k.shape[1]
+            k_in, k_shape = (B, Hk, N, d), (B, N, Hk, d)
+        else:
+            Hk = k.shape[2]
+            k_in, k_shape = (B, N, Hk, d), (B, Hk, N, d)
+        sk, there = _view("k", k, k_in, dtype, device)
+        here = here and there
     elif k_out is not None:
         raise ValueError("an output for k was given without k")
     rot = 0
     if freqs is not None:
-        _rank("freqs", freqs, 1)
+        if freqs.dim() != 1:
+            _rank("freqs", freqs, 1)
+        if freqs.dtype != torch.float64:
+            raise ValueError(f"freqs must be {torch.float64}, got {freqs.dtype}")
         rot = 2 * freqs.shape[0]
-        _expect("freqs", freqs, freqs.shape, torch.float64)
         if rot > d:
             raise ValueError(f"freqs rotates {rot} elements of a head of {d}")
-    if positions is not None and starts is not None:
-        raise ValueError("give positions or starts, not both")
+        here = here and freqs.device == device and freqs.is_contiguous()
     if positions is not None:
+        if starts is not None:
+            raise ValueError("give positions or starts, not both")
         _expect("positions", positions, (B, N), torch.int64)
-    if starts is not None:
+        here = here and positions.device == device and positions.is_contiguous()
+    elif starts is not None:
         _expect("starts", starts, (B,), torch.int64)
-    if layout not in ROTARY_LAYOUTS:
+        here = here and starts.device == device and starts.is_contiguous()
+    order = ROTARY_LAYOUTS.get(layout)
+    if order is None:
         raise ValueError(f"layout must be one of {tuple(ROTARY_LAYOUTS)}, got {layout!r}")
-    dt = _dt(q)
-    heads_first, heads_last = (B, Hq, N, d), (B, N, Hq, d)
-    shapes = [heads_first, (B, Hk, N, d), heads_last, (B, N, Hk, d)]
-    if not inverse:
-        shapes = shapes[2:] + shapes[:2]
-    sq = _view("q", q, shapes[0], dtype)
-    sk = None if k is None else _view("k", k, shapes[1], dtype)
-    sqo = None if q_out is None else _view("the output of q", q_out, shapes[2], dtype)
-    sko = None if k_out is None else _view("the output of k", k_out, shapes[3], dtype)
-    for t in (q, k, q_out, k_out):
-        if t is not None and (t.device != device or not t.is_cuda):
-            raise ValueError(f"tensors must be CUDA tensors on one device, got {device} and {t.device}")
-    for t in (freqs, positions, starts):
-        if t is not None and (t.device != device or not t.is_contiguous()):
-            raise ValueError(f"tables must be contiguous and on {device}, got {t.device}")
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _dt(q)
+    if q_out is not None:
+        sqo, there = _view("the output of q", q_out, q_shape, dtype, device)
+        here = here and there
+    if k_out is not None:
+        sko, there = _view("the output of k", k_out, k_shape, dtype, device)
+        here = here and there
+    if not here:
+        raise ValueError(f"tensors must be CUDA tensors on one device (q is on {device}), and the tables contiguous")
     away = _elsewhere(device, stream)
     if away is not None:
         with away:
             return _rotate(q, k, q_out, k_out, freqs, positions, starts, offset, layout, inverse, amplitude, q_scale,
                            k_scale, None)
     if q_out is None:
-        q_out = q.new_empty(shapes[2])
+        q_out = q.new_empty(q_shape)
         sqo = q_out.stride()
-    if k is None:
-        sk = sko = (0, 0, 0, 0)
-    elif k_out is None:
-        k_out = k.new_empty(shapes[3])
+    if k is not None and k_out is None:
+        k_out = k.new_empty(k_shape)
         sko = k_out.stride()
     n, h = (2, 1) if inverse else (1, 2)  # token and head dimension of the inputs; the outputs have them swapped
     strides = _Strides(sq[0], sq[n], sq[h], sk[0], sk[n], sk[h], sqo[0], sqo[h], sqo[n], sko[0], sko[h], sko[n])
     at = ctypes.addressof(strides)
     _check("ret_rotary",
-           load().ret_rotary(q.data_ptr(), _address(k), q_out.data_ptr(), _address(k_out), at, at + 24, at + 48, at + 72,
-                             _address(freqs), _address(positions), _address(starts), offset, B, N, Hq, Hk, d, rot,
-                             ROTARY_LAYOUTS[layout], inverse, amplitude, q_scale, k_scale, dt, _current_stream(device)))
+           (_lib or load()).ret_rotary(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                                       None if k is None else k_out.data_ptr(), at, at + 24, at + 48, at + 72,
+                                       None if freqs is None else freqs.data_ptr(), _address(positions),
+                                       _address(starts), int(offset), B, N, Hq, Hk, d, rot, order, inverse,
+                                       float(amplitude), float(q_scale), float(k_scale), dt, _current_stream(device)))
     return q_out, k_out
 
 
@@ -537,24 +570,31 @@ def rotary_backward(dq, dk, freqs, positions=None, starts=None, offset=0, layout
 
 
 def _norm_args(x, weight, bias):
-    """x [..., D]; weight and bias [D] of x's dtype or fp32, each or both None. Returns (rows, D, weight dtype)."""
-    shape = x.shape
+    """x [..., D]; weight and bias [D] of x's dtype or fp32, each or both None. Returns (shape, D, dtype,
+    weight dtype)."""
+    shape, dtype = x.shape, x.dtype
     if not shape:
         raise ValueError("x must have at least one dimension")
     D = shape[-1]
     if D == 0:
         raise ValueError(f"x must have rows of at least one element, got shape {tuple(shape)}")
-    _expect("weight", weight, (D,))
-    _expect("bias", bias, (D,))
-    w = weight if weight is not None else bias
-    if w is None:
-        return x.numel() // D, D, x.dtype
-    wdtype = w.dtype
-    if wdtype != torch.float32 and wdtype != x.dtype:
-        raise ValueError(f"weight and bias must be {x.dtype} or torch.float32, got {wdtype}")
-    if weight is not None and bias is not None and wdtype != bias.dtype:
-        raise ValueError(f"weight and bias must share one dtype, got {wdtype} and {bias.dtype}")
-    return x.numel() // D, D, wdtype
+    wdtype = None
+    if weight is not None:
+        wdtype = weight.dtype
+        if weight.shape != (D,):
+            _expect("weight", weight, (D,))
+    if bias is not None:
+        if bias.shape != (D,):
+            _expect("bias", bias, (D,))
+        if wdtype is None:
+            wdtype = bias.dtype
+        elif bias.dtype != wdtype:
+            raise ValueError(f"weight and bias must share one dtype, got {wdtype} and {bias.dtype}")
+    if wdtype is None:
+        wdtype = dtype
+    elif wdtype != torch.float32 and wdtype != dtype:
+        raise ValueError(f"weight and bias must be {dtype} or torch.float32, got {wdtype}")
+    return shape, D, dtype, wdtype
 
 
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, y=None, sum_out=None, mean=None,
@@ -563,22 +603,25 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, y=No
     None). Returns y. With a residual (x's shape and dtype) it normalises x + residual and returns
     (y, sum_out). mean and rstd (fp32, x's shape without D) receive the row statistics for
     layer_norm_backward if given. y and sum_out may each be the x or the residual tensor."""
-    rows, D, wdtype = _norm_args(x, weight, bias)
+    shape, D, dtype, wdtype = _norm_args(x, weight, bias)
     if residual is not None:
-        _expect("residual", residual, x.shape, x.dtype)
-    if y is not None:
-        _expect("y", y, x.shape, x.dtype)
-    if sum_out is not None:
-        _expect("sum_out", sum_out, x.shape, x.dtype)
-    if mean is not None:
-        _expect("mean", mean, x.shape[:-1], torch.float32)
-    if rstd is not None:
-        _expect("rstd", rstd, x.shape[:-1], torch.float32)
-    if sum_out is not None and residual is None:
+        _expect("residual", residual, shape, dtype)
+    elif sum_out is not None:
         raise ValueError("sum_out was given without a residual")
-    dt = _dt(x)
+    if y is not None:
+        _expect("y", y, shape, dtype)
+    if sum_out is not None:
+        _expect("sum_out", sum_out, shape, dtype)
+    if mean is not None:
+        _expect("mean", mean, shape[:-1], torch.float32)
+    if rstd is not None:
+        _expect("rstd", rstd, shape[:-1], torch.float32)
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _dt(x)
     _cuda(x, weight, bias, residual, y, sum_out, mean, rstd)
-    away = _elsewhere(x.device, stream)
+    device = x.device
+    away = _elsewhere(device, stream)
     if away is not None:
         with away:
             return layer_norm(x, weight, bias, eps, residual, y, sum_out, mean, rstd)
@@ -587,9 +630,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, y=No
     if residual is not None and sum_out is None:
         sum_out = torch.empty_like(x)
     _check("ret_layer_norm",
-           load().ret_layer_norm(x.data_ptr(), _address(residual), _address(weight), _address(bias), y.data_ptr(),
-                                 _address(sum_out), _address(mean), _address(rstd), rows, D, eps, dt,
-                                 RET_BF16 if wdtype == torch.bfloat16 else RET_F32, _current_stream(x.device)))
+           (_lib or load()).ret_layer_norm(x.data_ptr(), _address(residual), _address(weight), _address(bias),
+                                           y.data_ptr(), _address(sum_out), _address(mean), _address(rstd),
+                                           x.numel() // D, D, float(eps), dt, _DTYPES[wdtype], _current_stream(device)))
     return y if residual is None else (y, sum_out)
 
 
@@ -600,30 +643,41 @@ def layer_norm_backward(dy, x, weight, mean, rstd, dsum=None, dweight=True, dbia
     dx. Returns (dx, dweight, dbias), dweight None without a weight or with dweight=False, dbias None
     without dbias. dx may be the dy, x or dsum tensor. The dtype of dbias is the weight's, or wdtype
     (x's) where there is no weight."""
-    rows, D, wd = _norm_args(x, weight, None)
+    shape, D, dtype, wd = _norm_args(x, weight, None)
     if weight is None and wdtype is not None:
-        if wdtype not in (x.dtype, torch.float32):
-            raise ValueError(f"wdtype must be {x.dtype} or torch.float32, got {wdtype}")
+        if wdtype != dtype and wdtype != torch.float32:
+            raise ValueError(f"wdtype must be {dtype} or torch.float32, got {wdtype}")
         wd = wdtype
-    for name, t in (("dy", dy), ("dsum", dsum), ("dx", dx)):
-        _expect(name, t, x.shape, x.dtype)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _expect(name, t, x.shape[:-1], torch.float32)
-    dt = _dt(x)
+    _expect("dy", dy, shape, dtype)
+    if dsum is not None:
+        _expect("dsum", dsum, shape, dtype)
+    if dx is not None:
+        _expect("dx", dx, shape, dtype)
+    _expect("mean", mean, shape[:-1], torch.float32)
+    _expect("rstd", rstd, shape[:-1], torch.float32)
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        _dt(x)
     _cuda(dy, x, weight, mean, rstd, dsum, dx)
-    away = _elsewhere(x.device, stream)
+    device = x.device
+    away = _elsewhere(device, stream)
     if away is not None:
         with away:
             return layer_norm_backward(dy, x, weight, mean, rstd, dsum, dweight, dbias, wdtype, dx)
     if dx is None:
         dx = torch.empty_like(x)
     dw = torch.empty_like(weight) if dweight and weight is not None else None
-    db = x.new_empty(D, dtype=wd) if dbias else None
+    if not dbias:
+        db = None
+    elif weight is not None:
+        db = torch.empty_like(weight)
+    else:
+        db = x.new_empty(D, dtype=wd)
     _check("ret_layer_norm_backward",
-           load().ret_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _address(weight), mean.data_ptr(),
-                                          rstd.data_ptr(), _address(dsum), dx.data_ptr(), _address(dw), _address(db),
-                                          rows, D, dt, RET_BF16 if wd == torch.bfloat16 else RET_F32,
-                                          _current_stream(x.device)))
+           (_lib or load()).ret_layer_norm_backward(dy.data_ptr(), x.data_ptr(), _address(weight), mean.data_ptr(),
+                                                    rstd.data_ptr(), _address(dsum), dx.data_ptr(), _address(dw),
+                                                    _address(db), x.numel() // D, D, dt, _DTYPES[wd],
+                                                    _current_stream(device)))
     return dx, dw, db
 
 
