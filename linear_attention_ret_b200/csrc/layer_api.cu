@@ -20,7 +20,6 @@ constexpr int kMaxDevices = 64;
 
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-inline bool aligned16(const void* p) { return aligned_to(p, 16); }
 inline ret_status status(cudaError_t e) {
     if (e == cudaSuccess) return RET_OK;
     cudaGetLastError();  // reported by the status: nobody else's next check finds it
@@ -167,7 +166,7 @@ inline int rotary_units(const RotArgs& a, bool half, int ve) {
     return half ? a.rot / 2 / ve + ((a.d - a.rot) / ve + 1) / 2 : a.d / ve;
 }
 
-template <typename T, int VE, bool HALF, int BATCH>
+template <typename T, int VE, bool HALF, int BATCH, bool MANY>
 ret_status launch_rotary_batch(const RotArgs& a, int apart, cudaStream_t st) {
     constexpr int kTableBytes = 32 * 1024;  // most shared memory for cos and sin
     RotPlan pl;
@@ -180,24 +179,29 @@ ret_status launch_rotary_batch(const RotArgs& a, int apart, cudaStream_t st) {
     const long long all = (long long)a.B * a.N;
     // head groups of a token: one batch of rows per thread, or as many threads as there are heads
     // where that leaves SMs idle (decode)
-    int split = std::min(groups, (heads + BATCH - 1) / BATCH);
+    int split = MANY ? heads : std::min(groups, (heads + BATCH - 1) / BATCH);
     if (all * split < (long long)groups * 2 * sm_count()) split = std::min(groups, heads);
-    long long tokens = groups / split;
-    if (pl.stride) tokens = std::min<long long>(tokens, std::max(1, kTableBytes / (8 * pl.stride)));
-    pl.tokens = (int)std::min(tokens, all);
+    const int table = pl.stride ? std::max(1, kTableBytes / (8 * pl.stride)) : kRotThreads * BATCH;  // tokens it holds
+    pl.at_once = std::min(groups / split, MANY ? std::max(1, table / BATCH) : table);
+    pl.tokens = (int)std::min<long long>(MANY ? std::min(pl.at_once * BATCH, table) : pl.at_once, all);
     pl.units = FastDiv((unsigned)units);
     pl.split = FastDiv((unsigned)split);
     pl.N = FastDiv((unsigned)a.N);
     const size_t smem = (size_t)8 * pl.tokens * pl.stride;
-    return status(launch_dependent(rotary_vec_kernel<T, VE, HALF, BATCH>, (unsigned)((all + pl.tokens - 1) / pl.tokens),
-                                   kRotThreads, smem, st, a, pl));
+    return status(launch_dependent(rotary_vec_kernel<T, VE, HALF, BATCH, MANY>,
+                                   (unsigned)((all + pl.tokens - 1) / pl.tokens), kRotThreads, smem, st, a, pl));
 }
 
 template <typename T, int VE, bool HALF>
 ret_status launch_rotary_vec(const RotArgs& a, int apart, cudaStream_t st) {
+    const int heads = std::max(a.x[0].H, a.x[1].H), units = rotary_units(a, HALF, VE) * (a.x[1].H > 0 ? 2 : 1);
+    // few heads, a thread for each, and tokens enough for two blocks per SM all the same
+    if (heads < 4 && heads * units <= kRotThreads &&
+        (long long)a.B * a.N >= (long long)4 * (kRotThreads / (heads * units)) * 2 * sm_count())
+        return launch_rotary_batch<T, VE, HALF, 4, true>(a, apart, st);
     if constexpr (HALF && VE > 1)
-        if (std::max(a.x[0].H, a.x[1].H) >= 8) return launch_rotary_batch<T, VE, HALF, 8>(a, apart, st);
-    return launch_rotary_batch<T, VE, HALF, 4>(a, apart, st);
+        if (heads >= 8) return launch_rotary_batch<T, VE, HALF, 8, false>(a, apart, st);
+    return launch_rotary_batch<T, VE, HALF, 4, false>(a, apart, st);
 }
 
 // The widest vectors that every row of every view starts on and that the layout's parts are whole
@@ -445,8 +449,8 @@ ret_status launch_norm_backward_vec(const T* dy, const T* o, const T* gate, T* d
                                    (unsigned)rows));
 }
 
-// Rows in registers: whole 16-byte chunks on up to 32 lanes, or single elements on 32 lanes where
-// rows are not whole chunks; longer rows (and 2^30 rows and more) in two passes.
+// Rows in registers: whole 16-byte chunks on up to 32 lanes, or the narrower accesses of norm_vector
+// on 32 lanes; longer rows (and 2^30 rows and more) in two passes.
 template <typename T>
 ret_status launch_norm_gate_backward(const void* dy_, const void* o_, const void* gate_, void* dout_, void* dgate_,
                                      int B, int H, int N, int dv, float eps, cudaStream_t st) {
@@ -454,12 +458,11 @@ ret_status launch_norm_gate_backward(const void* dy_, const void* o_, const void
     const T *dy = static_cast<const T*>(dy_), *o = static_cast<const T*>(o_), *gate = static_cast<const T*>(gate_);
     T *dout = static_cast<T*>(dout_), *dgate = static_cast<T*>(dgate_);
     const size_t rows = (size_t)B * N * H;
-    const bool vec = dv % kE == 0 && aligned16(dy) && aligned16(o) && aligned16(gate) && aligned16(dout) &&
-                     aligned16(dgate);
+    const int ve = norm_vector(sizeof(T), 1, dv, {dy, o, gate, dout, dgate}, {});
 #define RET_NORM_BACKWARD(VE, LPR, CH) \
     if (dv <= VE * LPR * CH)           \
     return launch_norm_backward_vec<T, VE, LPR, CH>(dy, o, gate, dout, dgate, H, N, dv, eps, rows, st)
-    if (rows < (1u << 30) && vec) {
+    if (rows < (1u << 30) && ve == kE) {
         RET_NORM_BACKWARD(kE, 1, 1);
         RET_NORM_BACKWARD(kE, 2, 1);
         RET_NORM_BACKWARD(kE, 4, 1);
@@ -470,6 +473,15 @@ ret_status launch_norm_gate_backward(const void* dy_, const void* o_, const void
         RET_NORM_BACKWARD(kE, 32, 4);
         RET_NORM_BACKWARD(kE, 32, 8);
     } else if (rows < (1u << 30)) {
+        if constexpr (sizeof(T) == 2) {
+            if (ve == 2) {
+                RET_NORM_BACKWARD(2, 32, 1);
+                RET_NORM_BACKWARD(2, 32, 2);
+                RET_NORM_BACKWARD(2, 32, 4);
+                RET_NORM_BACKWARD(2, 32, 8);
+                RET_NORM_BACKWARD(2, 32, 16);
+            }
+        }
         RET_NORM_BACKWARD(1, 32, 2);
         RET_NORM_BACKWARD(1, 32, 4);
         RET_NORM_BACKWARD(1, 32, 8);

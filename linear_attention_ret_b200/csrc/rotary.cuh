@@ -55,7 +55,9 @@ __device__ __forceinline__ void rot_angle(const RotArgs& a, long long p, int i, 
 // two vectors, those whose elements pair up or two neighbours behind the rotated part. With VE = 1
 // (odd sizes and alignments) a unit is two elements in either layout. Threads of neighbouring
 // units and heads lie side by side, so a warp reads whole stretches of a token-major row. A block
-// holds `tokens` tokens of `split` head groups of q and of k each.
+// holds `tokens` tokens of `split` head groups of q and of k each. With fewer heads than BATCH
+// (MANY) each has its thread, and the thread's rows are of BATCH tokens, `at_once` apart: BATCH rows
+// are in flight either way, and what a block costs once is spread over as many.
 // cos and sin of a token are formed once per block, in shared memory, and serve all heads of q and
 // k; a thread's first BATCH rows are in flight meanwhile. HBM-bound; index arithmetic is once per
 // thread, as divisions per vector bound the kernel by instruction issue (1.3B-shaped, 134 MB:
@@ -63,7 +65,7 @@ __device__ __forceinline__ void rot_angle(const RotArgs& a, long long p, int i, 
 struct RotPlan {
     FastDiv units, split, N;  // units of a head; head groups of a token's q (or k); tokens of a batch
     int tensors;              // 2: q and k, 1: q alone
-    int tokens;               // of a block
+    int tokens, at_once;      // of a block; neighbouring threads' tokens
     int half_units;           // half layout, or VE = 1: units that are rotated
     int apart;                // and elements from the first of a pair to the second
     int stride;               // of a token's cos (or sin) in shared memory, in floats
@@ -75,47 +77,37 @@ struct RotUnit {
     static constexpr int P = HALF ? VE : VE / 2;  // frequencies of a unit
     typename V::Raw lo[BATCH], hi[HALF ? BATCH : 1];
 
-    // rows h, h + step, ... below H, at x and every `stride` elements; the second vector `second`
-    // elements on (half layout, 0: there is none)
-    __device__ __forceinline__ void load(const T* x, long long stride, int h, int step, int H, int second) {
-#pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            if (h + i * step < H) {
-                lo[i] = V::load_cs(x + i * stride);
-                if (HALF && second) hi[HALF ? i : 0] = V::load_cs(x + i * stride + second);
-            }
-        }
+    // row i at x; the second vector `second` elements on (half layout, 0: there is none)
+    __device__ __forceinline__ void load(int i, const T* x, int second) {
+        lo[i] = V::load_cs(x);
+        if (HALF && second) hi[HALF ? i : 0] = V::load_cs(x + second);
     }
 
     // live: how many of the unit's frequencies are rotated; c and s carry the scale m. Elements
     // that are not rotated are selected, not multiplied by 0: a neighbour may be infinite.
-    __device__ __forceinline__ void turn_store(T* y, long long stride, int h, int step, int H, int second, int live,
-                                               const float (&c)[P], const float (&s)[P], float m) {
+    __device__ __forceinline__ void turn_store(int i, T* y, int second, int live, const float (&c)[P], const float (&s)[P],
+                                               float m) {
+        float f[VE];
+        V::unpack(lo[i], f);
+        if (HALF) {
+            float g[VE];
+            V::unpack(hi[HALF ? i : 0], g);
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            if (h + i * step >= H) continue;
-            float f[VE];
-            V::unpack(lo[i], f);
-            if (HALF) {
-                float g[VE];
-                V::unpack(hi[HALF ? i : 0], g);
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    const float p = f[e], q = g[e];
-                    f[e] = live ? p * c[e % P] - q * s[e % P] : p * m;
-                    g[e] = live ? p * s[e % P] + q * c[e % P] : q * m;
-                }
-                if (second) V::store(y + i * stride + second, g);
-            } else {
-#pragma unroll
-                for (int e = 0; e < VE / 2; ++e) {
-                    const float p = f[2 * e], q = f[2 * e + 1];
-                    f[2 * e] = e < live ? p * c[e % P] - q * s[e % P] : p * m;
-                    f[2 * e + 1] = e < live ? p * s[e % P] + q * c[e % P] : q * m;
-                }
+            for (int e = 0; e < VE; ++e) {
+                const float p = f[e], q = g[e];
+                f[e] = live ? p * c[e % P] - q * s[e % P] : p * m;
+                g[e] = live ? p * s[e % P] + q * c[e % P] : q * m;
             }
-            V::store(y + i * stride, f);
+            if (second) V::store(y + second, g);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VE / 2; ++e) {
+                const float p = f[2 * e], q = f[2 * e + 1];
+                f[2 * e] = e < live ? p * c[e % P] - q * s[e % P] : p * m;
+                f[2 * e + 1] = e < live ? p * s[e % P] + q * c[e % P] : q * m;
+            }
         }
+        V::store(y, f);
     }
 };
 
@@ -123,7 +115,7 @@ struct RotUnit {
 // registers and leave three blocks on an SM instead of four (134 MB, 4 heads of 128: 26.9 us against
 // 25.9 us), and with eight heads or more a thread takes eight rows at once (gradient at the gated
 // layer's shapes, 268 MB: 47.0 us with four, 44.6 us with eight, 6.0 TB/s; the interleaved layout gains nothing).
-template <typename T, int VE, bool HALF, int BATCH>
+template <typename T, int VE, bool HALF, int BATCH, bool MANY>
 __global__ void __launch_bounds__(kRotThreads, BATCH > 4 ? 3 : 4) rotary_vec_kernel(const RotArgs a, const RotPlan pl) {
     using Unit = RotUnit<T, VE, HALF, BATCH>;
     constexpr int P = Unit::P;
@@ -138,21 +130,37 @@ __global__ void __launch_bounds__(kRotThreads, BATCH > 4 ? 3 : 4) rotary_vec_ker
     const bool second = pl.tensors == 2 && (t & 1);
     if (pl.tensors == 2) t >>= 1;
     const RotView& v = a.x[second];
-    const bool on = (int)t < tokens;
-    pl.N.divmod(first + t, b, n);
-    const int split = (int)pl.split.d, H = on ? v.H : 0;
+    const int split = (int)pl.split.d, H = v.H;
     const bool pair = HALF && (int)u < pl.half_units;
     // pairs next to each other lie like what is behind the rotated part: VE = 1, interleaved
     const int at = !HALF || (pair && pl.apart != 1) ? (int)u * VE
                                                     : (pair ? 0 : a.rot - 2 * VE * pl.half_units) + (int)u * 2 * VE;
     const int second_at = !HALF ? 0 : pair ? pl.apart : at + VE < a.d ? VE : 0;
     const int live = HALF ? (pair ? P : 0) : min(max(half - (int)u * P, 0), P);
-    const T* x = static_cast<const T*>(v.in) + b * v.ib + n * v.in_ + g * v.ih + at;
-    T* y = static_cast<T*>(v.out) + b * v.ob + n * v.on + g * v.oh + at;
     const long long si = split * v.ih, so = split * v.oh;
+    const float m = v.scale;
+    // threads behind the last group have no rows; t: MANY the first of the thread's tokens, else its only one
+    const bool on = (int)t < (MANY ? pl.at_once : tokens) && (!MANY || (int)g < H);
+    auto in_row = [&](unsigned token) {
+        pl.N.divmod(first + token, b, n);
+        return static_cast<const T*>(v.in) + b * v.ib + n * v.in_ + g * v.ih + at;
+    };
+    auto out_row = [&](unsigned token) {
+        pl.N.divmod(first + token, b, n);
+        return static_cast<T*>(v.out) + b * v.ob + n * v.on + g * v.oh + at;
+    };
+    const T* x = in_row(t);
+    T* y = out_row(t);
     wait_previous_kernel();
     Unit r;
-    r.load(x, si, (int)g, split, H, second_at);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+        if (MANY) {
+            if (on && (int)t + i * pl.at_once < tokens) r.load(i, in_row(t + i * pl.at_once), second_at);
+        } else if (on && (int)g + i * split < H) {
+            r.load(i, x + i * si, second_at);
+        }
+    }
     for (int j = threadIdx.x; j < tokens * half; j += kRotThreads) {
         const int tj = j / half, f = j - tj * half;
         unsigned bj, nj;
@@ -160,20 +168,39 @@ __global__ void __launch_bounds__(kRotThreads, BATCH > 4 ? 3 : 4) rotary_vec_ker
         rot_angle(a, rot_position(a, (int)bj, (int)nj), f, cs[tj * pl.stride + f], sn[tj * pl.stride + f]);
     }
     __syncthreads();
+    if (!on) return;
     float c[P], s[P];
-    const float m = v.scale;
+    auto angles = [&](unsigned token) {
 #pragma unroll
-    for (int e = 0; e < P; ++e) {
-        c[e] = on && e < live ? m * cs[t * pl.stride + u * P + e] : 0.f;
-        s[e] = on && e < live ? m * sn[t * pl.stride + u * P + e] : 0.f;
+        for (int e = 0; e < P; ++e) {
+            c[e] = e < live ? m * cs[token * pl.stride + u * P + e] : 0.f;
+            s[e] = e < live ? m * sn[token * pl.stride + u * P + e] : 0.f;
+        }
+    };
+    if (MANY) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const unsigned token = t + i * pl.at_once;
+            if ((int)token >= tokens) break;
+            angles(token);
+            r.turn_store(i, out_row(token), second_at, live, c, s, m);
+        }
+        return;
     }
+    angles(t);
     for (int h = (int)g;;) {
-        r.turn_store(y, so, h, split, H, second_at, live, c, s, m);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            if (h + i * split < H) r.turn_store(i, y + i * so, second_at, live, c, s, m);
+        }
         h += BATCH * split;
         if (h >= H) break;
         x += BATCH * si;
         y += BATCH * so;
-        r.load(x, si, h, split, H, second_at);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            if (h + i * split < H) r.load(i, x + i * si, second_at);
+        }
     }
 }
 
