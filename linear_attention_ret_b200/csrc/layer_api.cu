@@ -199,7 +199,7 @@ ret_status launch_rotary_vec(const RotArgs& a, int apart, cudaStream_t st) {
     if (heads < 4 && heads * units <= kRotThreads &&
         (long long)a.B * a.N >= (long long)4 * (kRotThreads / (heads * units)) * 2 * sm_count())
         return launch_rotary_batch<T, VE, HALF, 4, true>(a, apart, st);
-    if constexpr (HALF && VE > 1)
+    if constexpr (HALF && VE > 1 && VE * sizeof(T) <= 8)
         if (heads >= 8) return launch_rotary_batch<T, VE, HALF, 8, false>(a, apart, st);
     return launch_rotary_batch<T, VE, HALF, 4, false>(a, apart, st);
 }
