@@ -103,7 +103,9 @@ inline bool bytes_overlap(const void* a, size_t na, const void* b, size_t nb) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), z = reinterpret_cast<uintptr_t>(b);
     return a && b && x < z + nb && z < x + na;
 }
-inline bool ranges_overlap(const void* a, const void* b, size_t bytes) { return bytes_overlap(a, bytes, b, bytes); }
+inline bool ranges_overlap(const void* a, const void* b, size_t bytes) {
+    return bytes_overlap(a, bytes, b, bytes);
+}
 
 // ------------------------------------------------------------------ rotary prologue (see rotary.cuh)
 
@@ -286,39 +288,44 @@ int staying_blocks(Kernel kernel, StayingBlocks& known, int threads, size_t smem
     return (int)std::min<long long>(blocks, (long long)per_sm * sm_count());
 }
 
-template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD, bool RES>
+template <typename T, typename W, int VE, int EPT, bool WARP, bool RES, bool PAIR>
 ret_status launch_ln_forward(const T* x, const T* res, const W* w, const W* b, T* y, T* sum_out, float* mean,
                              float* rstd, long long rows, int D, float eps, cudaStream_t st) {
     static StayingBlocks known;
-    const int chunks = D / VE;
+    const int chunks = PAIR ? (D / VE + 1) / 2 : D / VE;  // of a block
     const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
     const int threads = WARP ? kLnThreads : lanes;
     const long long per_block = WARP ? threads / lanes : 1;
     const size_t smem = RowStream<T, VE, EPT, RES ? 2 : 1, 0>::bytes(threads);
-    const auto kernel = ln_forward_kernel<T, W, VE, EPT, WARP, HOLD, RES>;
-    const int grid = staying_blocks(kernel, known, threads, smem, (rows + per_block - 1) / per_block);
+    const auto kernel = ln_forward_kernel<T, W, VE, EPT, WARP, RES, PAIR>;
+    int grid = staying_blocks(kernel, known, threads, smem, (rows + per_block - 1) / per_block * (PAIR ? 2 : 1));
     if (grid == 0) return RET_ERR_CUDA;
-    return status(launch_dependent(kernel, (unsigned)grid, threads, smem, st, x, res, w, b, y, sum_out, mean, rstd,
-                                   (unsigned)rows, D, eps, lanes));
+    if (PAIR) grid = grid / 2 * 2;
+    return status(launch_clusters(kernel, (unsigned)grid, PAIR ? 2 : 1, threads, smem, st, x, res, w, b, y, sum_out,
+                                  mean, rstd, (unsigned)rows, D, eps, lanes));
 }
 
 template <typename T, typename W, int VE, bool RES>
 ret_status launch_ln_forward_width(const T* x, const T* res, const W* w, const W* b, T* y, T* sum_out, float* mean,
                                    float* rstd, long long rows, int D, float eps, cudaStream_t st) {
-#define RET_LN_FORWARD(LANES, EPT, WARP, HOLD) \
+#define RET_LN_FORWARD(LANES, EPT, WARP, PAIR) \
     if (D <= LANES * EPT)                      \
-    return launch_ln_forward<T, W, VE, EPT, WARP, HOLD, RES>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st)
-    RET_LN_FORWARD(32, 8, true, true);
-    RET_LN_FORWARD(32, 16, true, true);
-    RET_LN_FORWARD(512, 16, false, true);
-    if constexpr (RowStream<T, VE, 32, RES ? 2 : 1, 0>::bytes(512) <= kLnMaxShared)
+    return launch_ln_forward<T, W, VE, EPT, WARP, RES, PAIR>(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st)
+    RET_LN_FORWARD(32, 8, true, false);
+    RET_LN_FORWARD(32, 16, true, false);
+    RET_LN_FORWARD(512, 16, false, false);
+    using Wide = RowStream<T, VE, 32, RES ? 2 : 1, 0>;
+    if constexpr (Wide::kAsync && Wide::bytes(512) <= kLnMaxShared) {
         RET_LN_FORWARD(512, 32, false, false);
-    return RET_ERR_UNSUPPORTED;  // not reached: wider rows are not sent here
+    } else {
+        RET_LN_FORWARD(1024, 16, false, true);
+    }
 #undef RET_LN_FORWARD
+    return RET_ERR_UNSUPPORTED;  // not reached: wider rows are not sent here
 }
 
-// Rows of up to 8,192 elements (16,384 where two of them fit shared memory) are read once, in the
-// vectors of norm_vector; longer rows (and 2^30 rows and more) in three passes.
+// Rows of up to 16,384 elements are read once, in the vectors of norm_vector; longer rows (and 2^30
+// rows and more) in three passes.
 template <typename T, typename W>
 ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, const void* b_, void* y_,
                              void* sum_out_, float* mean, float* rstd, long long rows, int D, float eps,
@@ -327,8 +334,7 @@ ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, c
     const T *x = static_cast<const T*>(x_), *res = static_cast<const T*>(res_);
     const W *w = static_cast<const W*>(w_), *b = static_cast<const W*>(b_);
     T *y = static_cast<T*>(y_), *sum_out = static_cast<T*>(sum_out_);
-    constexpr bool kWideSum = RowStream<T, kE, 32, 2, 0>::bytes(512) <= kLnMaxShared;
-    if (D <= (res == nullptr || kWideSum ? 512 * 32 : 512 * 16) && rows < (1LL << 30)) {
+    if (D <= 1024 * 16 && rows < (1LL << 30)) {
         auto go = [&](auto plain, auto with_residual) {
             return (res ? with_residual : plain)(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
         };
@@ -409,7 +415,7 @@ ret_status launch_layer_norm_backward(const void* dy_, const void* x_, const voi
     const W* w = static_cast<const W*>(w_);
     T* dx = static_cast<T*>(dx_);
     W *dw = static_cast<W*>(dw_), *db = static_cast<W*>(db_);
-    if (D <= 2 * 512 * 16 && rows < (1LL << 30)) {
+    if (D <= 1024 * 16 && rows < (1LL << 30)) {
         auto go = [&](auto plain, auto with_sum) {
             return (dsum ? with_sum : plain)(dy, x, w, mean, rstd, dsum, dx, dw, db, rows, D, st);
         };

@@ -31,9 +31,11 @@ __device__ __forceinline__ void ln_weights(const W* w, float* f) {
 // to 16; a block holds `groups` of them, each with a row of its own. row_sum adds a value over a
 // row's threads, row_sums two at once; every thread gets the sums. Whole warps meet at a barrier
 // and take `sm`, one float per warp and value, zero behind the row's warps and not written again
-// before the next barrier. row_sum is for blocks of one group. row_sums' groups meet at barriers of
-// their own (number group + 1); a kernel with numbered barriers holds 16 of an SM's for each block, too
-// many where blocks are small (8192 x 1024 forward: 24.5 us against 13.6 us).
+// before the next barrier. PAIR: the row's threads are two blocks of a cluster; each warp's sums go
+// to both blocks' sm, and the cluster's barrier takes the place of the block's.
+// row_sum is for blocks of one group. row_sums' groups meet at barriers of their own (number
+// group + 1); a kernel with numbered barriers holds 16 of an SM's for each block, too many where
+// blocks are small (8192 x 1024 forward: 24.5 us against 13.6 us).
 struct RowThreads {
     int sub, lanes, group, groups;
     __device__ __forceinline__ void meet() const {
@@ -56,19 +58,28 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
-template <bool WARP>
+template <bool WARP, bool PAIR>
 __device__ __forceinline__ float row_sum(float v, const RowThreads& t, RowShared& sm) {
     if (WARP) return lanes_sum(v, t.lanes);
     v = lanes_sum<32>(v);
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, place = lane & (kLnWarps - 1);
+    if (PAIR) {
+        const cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+        if (lane == 0) {
+            float* mine = &sm[cluster.block_rank()][t.sub >> 5];
+            *mine = v;
+            *cluster.map_shared_rank(mine, cluster.block_rank() ^ 1) = v;
+        }
+        cluster.sync();
+        return lanes_sum<kLnWarps>(sm[0][place] + sm[1][place]);
+    }
     if (lane == 0) sm[0][t.sub >> 5] = v;
     __syncthreads();
-    return lanes_sum<kLnWarps>(sm[0][lane & (kLnWarps - 1)]);
+    return lanes_sum<kLnWarps>(sm[0][place]);
 }
 
 // Two sums for little more than the shuffles of one: after the first exchange the lower half of
-// a warp carries a and the upper half b. PAIR: the row's threads are two blocks of a cluster; each warp's
-// sums go to both blocks' sm, and the cluster's barrier takes the place of the block's.
+// a warp carries a and the upper half b.
 template <bool WARP, bool PAIR>
 __device__ __forceinline__ void row_sums(float& a, float& b, const RowThreads& t, RowShared (&sm)[PAIR ? 2 : 1]) {
     if (WARP && t.lanes < 32) {
@@ -284,36 +295,47 @@ __device__ __forceinline__ void column_weights(const W* w, float none, F2 (&f)[E
     for (int i = 0; i < EPT / 2; ++i) f[i] = F2(e[2 * i], e[2 * i + 1]);
 }
 
-// One row per `lanes` lanes of a warp (WARP), or per block; a thread keeps EPT elements of it: the
-// row is read once, and the mean and then the centred squares are summed from registers. Blocks
-// stay and take every gridDim.x-th row; the next row's loads are issued before the current
-// row's sums are reduced. HOLD: the thread's columns of weight and bias stay in registers too, else they
-// are read from L1 for every row.
-template <typename T, typename W, int VE, int EPT, bool WARP, bool HOLD, bool RES>
+// One row per `lanes` lanes of a warp (WARP), per block, or per pair of blocks of a cluster (PAIR, each
+// block with its columns); a thread keeps EPT elements of it: the row is read once, and the mean
+// and then the centred squares are summed from registers. Blocks stay and take every gridDim.x-th
+// row, with the next rows in flight and (EPT up to 16) their columns of weight and bias in
+// registers. HBM-bound at large sizes: 8192 x 2048 in bf16 (67 MB) 13.7 us, 4.9 TB/s; one row per block
+// and unpacked arithmetic took 23.9 us, two thirds of it instruction issue.
+// Above 8,192 elements a block of 512 threads takes EPT = 32 (1024 x 16384 in bf16: 20 us; a pair of
+// blocks, which meet twice a row, 35 us), or a pair does where the rows of EPT = 32 do not fit shared
+// memory (fp32 with a residual) or are single 2-byte elements, which wait in registers (184 x 9361
+// with a residual: 15 us against 20 us).
+template <typename T, typename W, int VE, int EPT, bool WARP, bool RES, bool PAIR>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
 ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y, T* sum_out,
                   float* mean, float* rstd, unsigned rows, int D, float eps, int lanes) {
     extern __shared__ uint4 ln_ring[];
     __shared__ RowShared sm[2][2];  // one group of whole warps
     const RowThreads t = row_threads(lanes);
-    const unsigned per_block = t.groups, mine = t.group, step = gridDim.x * per_block;
+    const unsigned blocks = PAIR ? gridDim.x / 2 : gridDim.x, block = PAIR ? blockIdx.x / 2 : blockIdx.x;
+    const unsigned per_block = t.groups, mine = t.group, step = blocks * per_block;
     const float inv = 1.f / (float)D;
+    // this block's columns
+    const int half = (D / VE + 1) / 2 * VE, left = PAIR ? (int)(blockIdx.x & 1) * half : 0;
+    const int width = !PAIR ? D : left ? D - half : half;
     if (!WARP) {
         for (int i = t.sub; i < 4 * 2 * kLnWarps; i += lanes) (&sm[0][0][0][0])[i] = 0.f;
     }
     wait_previous_kernel();
-    unsigned base = blockIdx.x * per_block;  // every group of a block makes the same trips
+    unsigned base = block * per_block;  // every group of a block makes the same trips
     RowStream<T, VE, EPT, RES ? 2 : 1, 0> in;
-    in.src[0] = x;
-    if (RES) in.src[RES] = res;
-    in.start(ln_ring, t, base + mine, step, rows, D, D);
-    size_t at = (size_t)(base + mine) * D + row_first<EPT / VE>(t) * VE;
+    in.src[0] = x + left;
+    if (RES) in.src[RES] = res + left;
+    in.start(ln_ring, t, base + mine, step, rows, D, width);
+    size_t at = (size_t)(base + mine) * D + left + row_first<EPT / VE>(t) * VE;
     F2 w[EPT / 2], b[EPT / 2];
-    if (HOLD) {
-        column_weights<W, VE, EPT>(weight, 1.f, w, t, D / VE);
-        column_weights<W, VE, EPT>(bias, 0.f, b, t, D / VE);
-    }
-    if (!WARP) __syncthreads();
+    auto columns = [&] {
+        column_weights<W, VE, EPT>(weight ? weight + left : weight, 1.f, w, t, width / VE);
+        column_weights<W, VE, EPT>(bias ? bias + left : bias, 0.f, b, t, width / VE);
+    };
+    if (EPT <= 16) columns();
+    if (PAIR) cooperative_groups::this_cluster().sync();
+    else if (!WARP) __syncthreads();
     for (int flip = 0; base < rows; base += step, at += in.stride, flip ^= 1) {
         const unsigned r = base + mine;
         F2 f[RES ? 2 : 1][EPT / 2];
@@ -327,7 +349,7 @@ ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y
         F2 q = v[0];
 #pragma unroll
         for (int i = 1; i < EPT / 2; ++i) q = add2(q, v[i]);
-        const float mu = row_sum<WARP>(q.sum(), t, sm[flip][0]) * inv;
+        const float mu = row_sum<WARP, PAIR>(q.sum(), t, sm[flip][0]) * inv;
         const F2 minus = F2(-mu, -mu);
         q = F2(0.f, 0.f);
 #pragma unroll
@@ -338,23 +360,21 @@ ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y
                                      in.has[(2 * i + 1) / VE] ? v[i].hi() - mu : 0.f);
             q = fma2(z, z, q);
         }
-        const float rs = rsqrtf(row_sum<WARP>(q.sum(), t, sm[flip][1]) * inv + eps);
+        const float rs = rsqrtf(row_sum<WARP, PAIR>(q.sum(), t, sm[flip][1]) * inv + eps);
         if (r < rows) {
             if (RES && sum_out) in.store(sum_out + at, v);
-            if (!HOLD) {
-                column_weights<W, VE, EPT>(weight, 1.f, w, t, D / VE);
-                column_weights<W, VE, EPT>(bias, 0.f, b, t, D / VE);
-            }
+            if (EPT > 16) columns();
             const F2 scale = F2(rs, rs);
 #pragma unroll
             for (int i = 0; i < EPT / 2; ++i) v[i] = fma2(mul2(add2(v[i], minus), scale), w[i], b[i]);
             in.store(y + at, v);
-            if (t.sub == 0) {
+            if (t.sub == 0 && left == 0) {
                 if (mean) mean[r] = mu;
                 if (rstd) rstd[r] = rs;
             }
         }
     }
+    if (PAIR) cooperative_groups::this_cluster().sync();  // the other block may still write its sums here
 }
 
 // dx and the column sums in one pass: blocks stay, and a thread keeps the same EPT columns of

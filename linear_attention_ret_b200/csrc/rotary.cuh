@@ -85,8 +85,8 @@ struct RotUnit {
 
     // live: how many of the unit's frequencies are rotated; c and s carry the scale m. Elements
     // that are not rotated are selected, not multiplied by 0: a neighbour may be infinite.
-    __device__ __forceinline__ void turn_store(int i, T* y, int second, int live, const float (&c)[P], const float (&s)[P],
-                                               float m) {
+    __device__ __forceinline__ void turn_store(int i, T* y, int second, int live, const float (&c)[P],
+                                               const float (&s)[P], float m) {
         float f[VE];
         V::unpack(lo[i], f);
         if (HALF) {
