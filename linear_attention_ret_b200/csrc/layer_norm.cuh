@@ -351,22 +351,24 @@ ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y
         for (int i = 1; i < EPT / 2; ++i) q = add2(q, v[i]);
         const float mu = row_sum<WARP, PAIR>(q.sum(), t, sm[flip][0]) * inv;
         const F2 minus = F2(-mu, -mu);
+        if (RES && sum_out && r < rows) in.store(sum_out + at, v);
         q = F2(0.f, 0.f);
 #pragma unroll
-        for (int i = 0; i < EPT / 2; ++i) {
-            // elements behind the row stay out of the sum of centred squares
-            const F2 z = VE > 1 ? (in.has[2 * i / VE] ? add2(v[i], minus) : F2(0.f, 0.f))
-                                : F2(in.has[2 * i / VE] ? v[i].lo() - mu : 0.f,
-                                     in.has[(2 * i + 1) / VE] ? v[i].hi() - mu : 0.f);
-            q = fma2(z, z, q);
+        for (int i = 0; i < EPT / 2; ++i) {  // elements behind the row stay out of the sum of centred squares
+            v[i] = add2(v[i], minus);
+            if (VE > 1) {
+                if (in.has[2 * i / VE]) q = fma2(v[i], v[i], q);
+            } else {
+                const F2 z = F2(in.has[2 * i / VE] ? v[i].lo() : 0.f, in.has[(2 * i + 1) / VE] ? v[i].hi() : 0.f);
+                q = fma2(z, z, q);
+            }
         }
         const float rs = rsqrtf(row_sum<WARP, PAIR>(q.sum(), t, sm[flip][1]) * inv + eps);
         if (r < rows) {
-            if (RES && sum_out) in.store(sum_out + at, v);
             if (EPT > 16) columns();
             const F2 scale = F2(rs, rs);
 #pragma unroll
-            for (int i = 0; i < EPT / 2; ++i) v[i] = fma2(mul2(add2(v[i], minus), scale), w[i], b[i]);
+            for (int i = 0; i < EPT / 2; ++i) v[i] = fma2(mul2(v[i], scale), w[i], b[i]);
             in.store(y + at, v);
             if (t.sub == 0 && left == 0) {
                 if (mean) mean[r] = mu;
