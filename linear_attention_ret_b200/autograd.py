@@ -6,7 +6,11 @@ the Gated RetNet page's parallel_gate_retention weights for the gated form).
 
 The operators around retention in the same manner: rotary (the prologue), msr_norm_gate (the
 epilogue) and layer_norm; multi_scale_retention runs prologue, retention and epilogue. Their
-gradients are not differentiable again: a second backward raises."""
+gradients are not differentiable again: a second backward raises.
+
+Capturing a backward in a CUDA graph: take the gradients with torch.autograd.grad, and let go of
+eager graphs over the same leaves first. backward() accumulates into the leaves on the stream on
+which an earlier graph met them, which a capture on another stream cannot wait for."""
 from __future__ import annotations
 
 import torch
