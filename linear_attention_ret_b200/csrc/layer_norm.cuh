@@ -295,20 +295,20 @@ __device__ __forceinline__ void column_weights(const W* w, float none, F2 (&f)[E
     for (int i = 0; i < EPT / 2; ++i) f[i] = F2(e[2 * i], e[2 * i + 1]);
 }
 
-// One row per `lanes` lanes of a warp (WARP), per block, or per pair of blocks of a cluster (PAIR, each
-// block with its columns); a thread keeps EPT elements of it: the row is read once, and the mean
-// and then the centred squares are summed from registers. Blocks stay and take every gridDim.x-th
-// row, with the next rows in flight and (EPT up to 16) their columns of weight and bias in
-// registers. HBM-bound at large sizes: 8192 x 2048 in bf16 (67 MB) 13.7 us, 4.9 TB/s; one row per block
-// and unpacked arithmetic took 23.9 us, two thirds of it instruction issue.
+// One row per `lanes` lanes of a warp (WARP), per block, or per pair of blocks of a cluster (PAIR,
+// each block with its columns); a thread keeps EPT elements of it: the row is read once, and the
+// mean and then the centred squares are summed from registers. Blocks stay and take every
+// gridDim.x-th row, with the next rows in flight and (EPT up to 16) their columns of weight and bias
+// in registers. HBM-bound at large sizes: 8192 x 2048 in bf16 (67 MB) 13.6 us, 4.9 TB/s; one row
+// per block and unpacked arithmetic took 23.9 us, two thirds of it instruction issue.
 // Above 8,192 elements a block of 512 threads takes EPT = 32 (1024 x 16384 in bf16: 20 us; a pair of
 // blocks, which meet twice a row, 35 us), or a pair does where the rows of EPT = 32 do not fit shared
 // memory (fp32 with a residual) or are single 2-byte elements, which wait in registers (184 x 9361
 // with a residual: 15 us against 20 us).
 template <typename T, typename W, int VE, int EPT, bool WARP, bool RES, bool PAIR>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
-ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y, T* sum_out,
-                  float* mean, float* rstd, unsigned rows, int D, float eps, int lanes) {
+ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y, T* sum_out, float* mean, float* rstd,
+                  unsigned rows, int D, float eps, int lanes) {
     extern __shared__ uint4 ln_ring[];
     __shared__ RowShared sm[2][2];  // one group of whole warps
     const RowThreads t = row_threads(lanes);
@@ -379,21 +379,23 @@ ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y
     if (PAIR) cooperative_groups::this_cluster().sync();  // the other block may still write its sums here
 }
 
-// dx and the column sums in one pass: blocks stay, and a thread keeps the same EPT columns of
-// every row it takes, their dw and db sums in registers. The next row's loads are issued before
-// the current row's two sums are reduced. Each block ends with one row of partial sums, part
-// [gridDim.x, 2, ln_pitch(D)]; ln_reduce_kernel adds those in order.
+// Floats of one row of column sums: a multiple of four, so that rows start on 16 bytes.
 __host__ __device__ constexpr int ln_pitch(int D) { return (D + 3) / 4 * 4; }
 
-//
-// PAIR: rows too wide for the registers of one block's 512 threads are split over the two blocks
-// of a cluster, each with its columns. Two blocks of 512 threads hold 16,384 columns; a second pass over the
-// rows for the column sums took 95 us at 1024 x 16384 in bf16 (100 MB).
+// dx and the column sums in one pass: blocks stay, and a thread keeps the same EPT columns of
+// every row it takes, their dw and db sums in registers; the next rows are in flight. Groups of
+// whole warps share a block of 512 threads, one row each, and join their column sums at the end:
+// each block leaves one row of partial sums, part [blocks, 2, ln_pitch(D)], which ln_reduce_kernel
+// adds in order. HBM-bound: 8192 x 4096 in bf16 with the sum's gradient (269 MB) 48.4 us with the
+// reduction, 5.5 TB/s; dx and the column sums in a pass each took 228 us. Joining partial sums over
+// clusters instead was slower (8192 x 2048: 38.4 us against 27.7 us).
+// PAIR: rows too wide for the registers of one block are split over the two blocks of a cluster, each
+// with its columns (1024 x 16384 in bf16, 100 MB: 39 us, bound by the cluster's barrier in every
+// row; 95 us with a second pass for the column sums).
 template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM, bool PAIR>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
-ln_backward_kernel(const T* dy, const T* x, const W* weight, const float* mean,
-                   const float* rstd, const T* dsum, T* dx, float* part, unsigned rows, int D,
-                   int lanes) {
+ln_backward_kernel(const T* dy, const T* x, const W* weight, const float* mean, const float* rstd, const T* dsum, T* dx,
+                   float* part, unsigned rows, int D, int lanes) {
     constexpr int P = EPT / 2;
     extern __shared__ uint4 ln_ring[];  // rows in flight, and at the end column sums
     __shared__ RowShared sm_all[WARP || PAIR ? 1 : kLnGroups][2][PAIR ? 2 : 1];
@@ -460,8 +462,8 @@ ln_backward_kernel(const T* dy, const T* x, const W* weight, const float* mean,
     }
     if (PAIR) cooperative_groups::this_cluster().sync();  // the other block may still write its sums here
     if (!part) return;
-    // column sums to shared memory, [2, Dp]: the groups of a warp (WARP) joined first, then one warp or
-    // group after another
+    // column sums to shared memory, [2, Dp]: the groups of a warp (WARP) joined first, then one warp
+    // or group after another
     __syncthreads();  // no copy is in flight: every row that was issued has been taken
     float* acc = reinterpret_cast<float*>(ln_ring);
     const int Dp = ln_pitch(D);
