@@ -89,7 +89,8 @@ cudaError_t launch_clusters(void (*kernel)(P...), unsigned grid, int cluster, in
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
 }
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st,
+                             A&&... args) {
     return launch_clusters(kernel, grid, 1, threads, smem, st, std::forward<A>(args)...);
 }
 
@@ -293,10 +294,10 @@ ret_status launch_ln_forward(const T* x, const T* res, const W* w, const W* b, T
                              float* rstd, long long rows, int D, float eps, cudaStream_t st) {
     static StayingBlocks known;
     const int chunks = PAIR ? (D / VE + 1) / 2 : D / VE;  // of a block
-    const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
+    const int lanes = WARP ? (VE == 1 ? 32 : lanes_for(chunks)) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
     const int threads = WARP ? kLnThreads : lanes;
     const long long per_block = WARP ? threads / lanes : 1;
-    const size_t smem = RowStream<T, VE, EPT, RES ? 2 : 1, 0>::bytes(threads);
+    const size_t smem = Rows<T, VE, EPT, RES ? 2 : 1, 0>::bytes(threads);
     const auto kernel = ln_forward_kernel<T, W, VE, EPT, WARP, RES, PAIR>;
     int grid = staying_blocks(kernel, known, threads, smem, (rows + per_block - 1) / per_block * (PAIR ? 2 : 1));
     if (grid == 0) return RET_ERR_CUDA;
@@ -314,7 +315,7 @@ ret_status launch_ln_forward_width(const T* x, const T* res, const W* w, const W
     RET_LN_FORWARD(32, 8, true, false);
     RET_LN_FORWARD(32, 16, true, false);
     RET_LN_FORWARD(512, 16, false, false);
-    using Wide = RowStream<T, VE, 32, RES ? 2 : 1, 0>;
+    using Wide = Rows<T, VE, 32, RES ? 2 : 1, 0>;
     if constexpr (Wide::kAsync && Wide::bytes(512) <= kLnMaxShared) {
         RET_LN_FORWARD(512, 32, false, false);
     } else {
@@ -359,14 +360,14 @@ template <typename T, typename W, int VE, int EPT, bool WARP, bool SUM, bool PAI
 ret_status launch_ln_backward(const T* dy, const T* x, const W* w, const float* mean, const float* rstd, const T* dsum,
                               T* dx, W* dw, W* db, long long rows, int D, cudaStream_t st) {
     const int chunks = PAIR ? (D / VE + 1) / 2 : D / VE;  // of a block
-    const int lanes = WARP ? lanes_for(chunks) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
+    const int lanes = WARP ? (VE == 1 ? 32 : lanes_for(chunks)) : warp_threads((chunks + EPT / VE - 1) / (EPT / VE));
     // rows at once: a warp's groups of lanes, one row per pair of blocks, or groups of whole warps up
     // to 512 threads as far as there are rows for them
     int groups = WARP ? kLnThreads / lanes : 1;
     if (!WARP && !PAIR)
         groups = (int)std::max<long long>(1, std::min<long long>(std::min(kLnGroups, 512 / lanes), rows / sm_count()));
     const int threads = groups * lanes;
-    const size_t ring = RowStream<T, VE, EPT, SUM ? 3 : 2, 2>::bytes(threads);
+    const size_t ring = Rows<T, VE, EPT, SUM ? 3 : 2, 2>::bytes(threads);
     const size_t smem = std::max(ring, sizeof(float) * 2 * ln_pitch(D));
     static StayingBlocks known;
     const auto kernel = ln_backward_kernel<T, W, VE, EPT, WARP, SUM, PAIR>;

@@ -11,6 +11,7 @@
 #pragma once
 
 #include <cooperative_groups.h>
+#include <type_traits>
 
 #include "vec.cuh"
 
@@ -212,7 +213,7 @@ struct RowStream {
     // src and stat are set; issues the first kAhead rows. The stream is of the first `width` of
     // rows of D elements.
     __device__ __forceinline__ void start(void* smem, const RowThreads& t, unsigned row, unsigned step_, unsigned rows_,
-                                          int D, int width) {
+                                          int D, int width, int) {
         const int chunks = width / VE;
         next = row;
         step = step_;
@@ -265,6 +266,8 @@ struct RowStream {
         }
         issue();
     }
+    static constexpr bool full = false;
+    __device__ __forceinline__ bool in_row(int e) const { return has[e / VE]; }  // this thread's element e
     __device__ __forceinline__ void store(T* row, const F2 (&f)[EPT / 2]) const {  // row: this thread's first vector
         float e[EPT];
 #pragma unroll
@@ -278,6 +281,156 @@ struct RowStream {
         }
     }
 };
+
+// The same for single elements (VE = 1): a warp copies the 16-byte units that cover its stretch of 32
+// EPT elements, and its threads then read single elements of them, neighbouring lanes neighbouring
+// elements. Copies are wide and asynchronous whatever a row starts on; a unit that reaches over
+// either end of the tensor is filled element by element. Units hold neighbours' elements too, which
+// an in-place call may be writing: they are copied and never looked at.
+template <typename T, int EPT, int N, int N_STAT>
+struct RowSpan {
+    static constexpr bool kAsync = true;
+    static constexpr int E = 16 / (int)sizeof(T);  // elements of a unit
+    static constexpr int kRowBytes = N * EPT * (int)sizeof(T);
+    static constexpr int kSlots = kRowBytes <= 64 ? 4 : kRowBytes <= 128 ? 3 : 2;
+    static constexpr int kAhead = kSlots - 1;
+    static constexpr int kUnits = 32 * EPT / E + 1;  // most units that a warp's stretch touches
+    static constexpr size_t bytes(int threads) { return (size_t)kSlots * N * (threads / 32) * kUnits * 16; }
+
+    const T* src[N];  // of this warp's first element of the next row to copy (start: of the tensors)
+    const float* stat[N_STAT > 0 ? N_STAT : 1];
+    unsigned next, step, rows;  // the next row to copy
+    long long stride;           // elements from a row to the next of this warp
+    int left;                   // this thread's element c is in the row where 32 c < left
+    bool full;                  // all of the warp's elements are (asked first: one test for sixteen)
+    const T *begin[N], *end[N];  // of the tensors
+    T* slots;                    // this warp's place in slot 0
+    int put, get;                // the slot to fill and the slot to read next
+    int pitch;                   // elements from a slot's tensor to the next
+    int count;                   // elements of this warp's stretch
+    int skip[N];                 // elements before the current row's first in its first unit
+    float stats[2][N_STAT > 0 ? N_STAT : 1];  // of the current row and the next
+    unsigned next_stat;
+
+    static __device__ __forceinline__ int off_unit(const T* p) {
+        return (int)(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & (E - 1);
+    }
+    __device__ __forceinline__ void issue() {
+        if (next < rows) {
+            const int lane = threadIdx.x & 31;
+            // rows whose units may reach over an end (they may be shorter than a unit)
+            const bool edge = next < (unsigned)E || next + E >= rows;
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                const int off = off_unit(src[t]), units = count > 0 ? (off + count + E - 1) / E : 0;
+                const T* from = src[t] - off;
+                T* to = slots + (put * N + t) * pitch;
+#pragma unroll
+                for (int j = 0; j < (kUnits + 31) / 32; ++j) {
+                    const int u = j * 32 + lane;
+                    if (u >= units) continue;
+                    const T* p = from + u * E;
+                    if (edge && (p < begin[t] || p + E > end[t])) {
+                        for (int e = 0; e < E; ++e)
+                            if (p + e >= begin[t] && p + e < end[t]) to[u * E + e] = p[e];
+                    } else {
+                        copy_async<16>(to + u * E, p);
+                    }
+                }
+                src[t] += stride;
+            }
+            next += step;
+        }
+        copy_commit();
+        put = put == kSlots - 1 ? 0 : put + 1;
+    }
+    __device__ __forceinline__ void load_stats(float (&s)[N_STAT > 0 ? N_STAT : 1]) {
+#pragma unroll
+        for (int k = 0; k < N_STAT; ++k) s[k] = next_stat < rows ? stat[k][next_stat] : 0.f;
+        next_stat += step;
+    }
+    // tensors: src as given, rows_ rows of D elements from `before` elements before src on
+    __device__ __forceinline__ void start(void* smem, const RowThreads& t, unsigned row, unsigned step_, unsigned rows_,
+                                          int D, int width, int before) {
+        next = row;
+        step = step_;
+        rows = rows_;
+        stride = (long long)step * D;
+        const int first = (t.sub >> 5) * 32 * EPT;
+        count = min(32 * EPT, width - first);
+        pitch = (blockDim.x / 32) * kUnits * E;
+        slots = static_cast<T*>(smem) + (threadIdx.x >> 5) * kUnits * E;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            begin[k] = src[k] - before;
+            end[k] = begin[k] + (size_t)rows * D;
+            src[k] += row < rows ? (size_t)row * D + first : 0;
+            skip[k] = off_unit(src[k]);
+        }
+        next_stat = row;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) load_stats(stats[k]);
+        put = get = 0;
+        left = count - (t.sub & 31);
+        full = count == 32 * EPT;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) issue();
+    }
+    __device__ __forceinline__ void take(F2 (&f)[N][EPT / 2], float (&s)[N_STAT > 0 ? N_STAT : 1]) {
+        if (N_STAT > 0) {
+#pragma unroll
+            for (int k = 0; k < N_STAT; ++k) {
+                s[k] = stats[0][k];
+                stats[0][k] = stats[1][k];
+            }
+            load_stats(stats[1]);
+        }
+        copy_wait<kAhead - 1>();
+        __syncwarp();  // every lane's copies have landed, and every lane has read the slot that is filled next
+#pragma unroll
+        for (int t = 0; t < N; ++t) {
+            const T* from = slots + (get * N + t) * pitch + skip[t] + (threadIdx.x & 31);
+            float e[EPT];
+            if (full) {
+#pragma unroll
+                for (int c = 0; c < EPT; ++c) e[c] = ld_elem(from + c * 32);
+            } else {
+#pragma unroll
+                for (int c = 0; c < EPT; ++c) e[c] = 32 * c < left ? ld_elem(from + c * 32) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < EPT / 2; ++i) f[t][i] = F2(e[2 * i], e[2 * i + 1]);
+            skip[t] = (skip[t] + (int)(stride & (E - 1))) & (E - 1);
+        }
+        get = get == kSlots - 1 ? 0 : get + 1;
+        issue();
+    }
+    __device__ __forceinline__ bool in_row(int e) const { return 32 * e < left; }
+    __device__ __forceinline__ void store(T* row, const F2 (&f)[EPT / 2]) const {  // row: this thread's first element
+        if (full) {
+#pragma unroll
+            for (int c = 0; c < EPT; ++c) st_elem(row + c * 32, c & 1 ? f[c / 2].hi() : f[c / 2].lo());
+        } else {
+#pragma unroll
+            for (int c = 0; c < EPT; ++c)
+                if (32 * c < left) st_elem(row + c * 32, c & 1 ? f[c / 2].hi() : f[c / 2].lo());
+        }
+    }
+};
+
+// Single elements are read through spans where that was faster: the forward of fp32 (9189 x 1023 with a
+// residual: 27.5 us against 32.2 us), the backward of fp32 with three tensors (16400 x 1023: 51.2 us
+// against 61.9 us; with two 55.7 us against 51.2 us) and, of either type, the backward's rows above 4,096
+// elements (2048 x 8191 in bf16: 38.6 us against 62.7 us). Elsewhere bf16 waits in registers (16400 x
+// 1023: forward 26.8 us against 30.8 us, backward 33.4 us against 55.5 us).
+template <typename T, int VE, int EPT, int N, int N_STAT>
+constexpr bool by_span() {
+    if (VE > 1) return false;
+    return N_STAT == 0 ? sizeof(T) == 4 : EPT > 8 || (sizeof(T) == 4 && N == 3);
+}
+template <typename T, int VE, int EPT, int N, int N_STAT>
+using Rows = std::conditional_t<by_span<T, VE, EPT, N, N_STAT>(), RowSpan<T, EPT, N, N_STAT>,
+                                RowStream<T, VE, EPT, N, N_STAT>>;
 
 // Pairs of a thread's columns of a weight, `none` where there is no weight or no column.
 template <typename W, int VE, int EPT>
@@ -303,8 +456,7 @@ __device__ __forceinline__ void column_weights(const W* w, float none, F2 (&f)[E
 // per block and unpacked arithmetic took 23.9 us, two thirds of it instruction issue.
 // Above 8,192 elements a block of 512 threads takes EPT = 32 (1024 x 16384 in bf16: 20 us; a pair of
 // blocks, which meet twice a row, 35 us), or a pair does where the rows of EPT = 32 do not fit shared
-// memory (fp32 with a residual) or are single 2-byte elements, which wait in registers (184 x 9361
-// with a residual: 15 us against 20 us).
+// memory (fp32 with a residual).
 template <typename T, typename W, int VE, int EPT, bool WARP, bool RES, bool PAIR>
 __global__ void __launch_bounds__(WARP ? kLnThreads : 512)
 ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y, T* sum_out, float* mean, float* rstd,
@@ -323,10 +475,10 @@ ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y
     }
     wait_previous_kernel();
     unsigned base = block * per_block;  // every group of a block makes the same trips
-    RowStream<T, VE, EPT, RES ? 2 : 1, 0> in;
+    Rows<T, VE, EPT, RES ? 2 : 1, 0> in;
     in.src[0] = x + left;
     if (RES) in.src[RES] = res + left;
-    in.start(ln_ring, t, base + mine, step, rows, D, width);
+    in.start(ln_ring, t, base + mine, step, rows, D, width, left);
     size_t at = (size_t)(base + mine) * D + left + row_first<EPT / VE>(t) * VE;
     F2 w[EPT / 2], b[EPT / 2];
     auto columns = [&] {
@@ -356,10 +508,10 @@ ln_forward_kernel(const T* x, const T* res, const W* weight, const W* bias, T* y
 #pragma unroll
         for (int i = 0; i < EPT / 2; ++i) {  // elements behind the row stay out of the sum of centred squares
             v[i] = add2(v[i], minus);
-            if (VE > 1) {
-                if (in.has[2 * i / VE]) q = fma2(v[i], v[i], q);
+            if (VE > 1 || in.full) {
+                if (in.full || in.in_row(2 * i)) q = fma2(v[i], v[i], q);
             } else {
-                const F2 z = F2(in.has[2 * i / VE] ? v[i].lo() : 0.f, in.has[(2 * i + 1) / VE] ? v[i].hi() : 0.f);
+                const F2 z = F2(in.in_row(2 * i) ? v[i].lo() : 0.f, in.in_row(2 * i + 1) ? v[i].hi() : 0.f);
                 q = fma2(z, z, q);
             }
         }
@@ -413,13 +565,13 @@ ln_backward_kernel(const T* dy, const T* x, const W* weight, const float* mean, 
     allow_next_kernel();
     wait_previous_kernel();
     unsigned base = block * per_block;  // every group of a block makes the same trips
-    RowStream<T, VE, EPT, SUM ? 3 : 2, 2> in;
+    Rows<T, VE, EPT, SUM ? 3 : 2, 2> in;
     in.src[0] = dy + left;
     in.src[1] = x + left;
     if (SUM) in.src[SUM ? 2 : 0] = dsum + left;
     in.stat[0] = mean;
     in.stat[1] = rstd;
-    in.start(ln_ring, t, base + mine, step, rows, D, width);
+    in.start(ln_ring, t, base + mine, step, rows, D, width, left);
     size_t at = (size_t)(base + mine) * D + left + row_first<EPT / VE>(t) * VE;
     F2 w[P], dw[P], db[P];
     column_weights<W, VE, EPT>(weight ? weight + left : weight, 1.f, w, t, width / VE);
@@ -487,7 +639,7 @@ ln_backward_kernel(const T* dy, const T* x, const W* weight, const float* mean, 
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int e = 2 * i + k, at_col = (row_first<EPT / VE>(t) + e / VE * 32) * VE + e % VE;
-                    if (!in.has[e / VE]) continue;
+                    if (!in.in_row(e)) continue;
                     const float a = k ? dw[i].hi() : dw[i].lo(), d = k ? db[i].hi() : db[i].lo();
                     acc[at_col] = q ? acc[at_col] + a : a;
                     acc[Dp + at_col] = q ? acc[Dp + at_col] + d : d;

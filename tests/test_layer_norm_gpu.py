@@ -20,7 +20,7 @@ def randn(*shape, dtype=f32, seed=0, shift=0.0):
 
 
 # rows, D: one row, few rows, many; widths of one vector, below and above each kernel's reach, and odd ones
-SIZES = [(1, 1), (3, 2), (5, 8), (1, 64), (7, 100), (65, 127), (9, 256), (300, 512), (33, 771), (17, 1023), (64, 1024),
+SIZES = [(1, 1), (20, 1), (3, 2), (21, 3), (2, 7), (5, 8), (1, 64), (7, 100), (65, 127), (9, 256), (300, 512), (33, 771), (17, 1023), (64, 1024),
          (1000, 1280), (40, 2048), (13, 2050), (129, 4096), (5, 5000), (37, 8192), (3, 8191), (4, 16384), (2, 16380)]
 TYPES = [(bf, bf), (bf, f32), (f32, f32)]
 
@@ -170,6 +170,19 @@ def test_backward_in_place(cuda_lib, rows, D):
         out = cuda_lib.layer_norm_backward(t["dy"], t["x"], w, mean, rstd, dsum=t["dsum"], dx=t[place])
         assert out[0].data_ptr() == t[place].data_ptr()
         assert all(torch.equal(a, g) for a, g in zip(out, got)), place
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("rows,D", [(300, 1023), (40, 5), (150, 6001)])
+def test_in_place_at_odd_widths(cuda_lib, rows, D, dtype):
+    """Rows that start on no 16 bytes share units of memory with their neighbours."""
+    dy, x, w, mean, rstd, dsum, got = backward_check(cuda_lib, rows, D, dtype, f32, residual=True)
+    out = cuda_lib.layer_norm_backward(dy, x, w, mean, rstd, dsum=dsum, dx=dy)
+    assert all(torch.equal(a, g) for a, g in zip(out, got))
+    y, s = cuda_lib.layer_norm(x, w, residual=dsum)
+    a, c = x.clone(), dsum.clone()
+    cuda_lib.layer_norm(a, w, residual=c, y=a, sum_out=c)
+    assert torch.equal(a, y) and torch.equal(c, s)
 
 
 def test_no_rows(cuda_lib):
