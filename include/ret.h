@@ -333,7 +333,8 @@ RET_API ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k
  * Layer norm of each of `rows` contiguous rows of D elements, the norm in front of a RetNet
  * block's retention and feed-forward sub-layers:
  *   s = x (+ residual),  y = weight * (s - mean_c s) / sqrt(mean_c (s - mean_c s)^2 + eps) + bias.
- *   x, y          [rows, D] of type dt; residual and sum_out (s, rounded to dt) likewise, or NULL.
+ *   x, y          [rows, D] of type dt; residual and sum_out (s, rounded to dt; without a residual a
+ *                 copy of x) likewise, each or both NULL.
  *   weight, bias  [D] of type wdt (dt or RET_F32), each or both NULL (1 and 0).
  *   mean, rstd    [rows] fp32, the row statistics for the backward pass, or NULL.
  * Statistics are fp32, of centred values, and with a residual of the unrounded sum. y and

@@ -326,7 +326,9 @@ ret_status launch_ln_forward_width(const T* x, const T* res, const W* w, const W
 }
 
 // Rows of up to 16,384 elements are read once, in the vectors of norm_vector; longer rows (and 2^30
-// rows and more) in three passes.
+// rows and more) in three passes. So is a sum without a residual, which is x: the one-pass kernels store
+// a sum only where they form one. With that store in those without a residual too, calls that ask for no
+// sum took longer above 8,192 elements (2046 x 8200 in bf16: 24.8 us against 20.2 us).
 template <typename T, typename W>
 ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, const void* b_, void* y_,
                              void* sum_out_, float* mean, float* rstd, long long rows, int D, float eps,
@@ -335,7 +337,7 @@ ret_status launch_layer_norm(const void* x_, const void* res_, const void* w_, c
     const T *x = static_cast<const T*>(x_), *res = static_cast<const T*>(res_);
     const W *w = static_cast<const W*>(w_), *b = static_cast<const W*>(b_);
     T *y = static_cast<T*>(y_), *sum_out = static_cast<T*>(sum_out_);
-    if (D <= 1024 * 16 && rows < (1LL << 30)) {
+    if (D <= 1024 * 16 && rows < (1LL << 30) && (res || !sum_out)) {
         auto go = [&](auto plain, auto with_residual) {
             return (res ? with_residual : plain)(x, res, w, b, y, sum_out, mean, rstd, rows, D, eps, st);
         };

@@ -675,8 +675,8 @@ __device__ __forceinline__ float block_sum(float x, float* sm) {
 template <typename W>
 __device__ __forceinline__ float ln_weight(const W* w, int c, float none) { return w ? ld_elem(w + c) : none; }
 
-// Any D: one block per row, three passes (the later ones from L1/L2). x, residual, y and
-// sum_out may alias element by element: an element is read by the thread that writes it.
+// Any D, and a sum without a residual: one block per row, three passes (the later ones from L1/L2). x,
+// residual, y and sum_out may alias element by element: an element is read by the thread that writes it.
 template <typename T, typename W>
 __global__ void __launch_bounds__(kLnThreads)
 ln_forward_rows_kernel(const T* x, const T* res, const W* __restrict__ weight, const W* __restrict__ bias, T* y,
