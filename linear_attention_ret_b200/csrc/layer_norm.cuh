@@ -10,6 +10,7 @@
 // fp32 sum, not of its rounded copy: one rounding less, at no cost.
 #pragma once
 
+#include <cfloat>
 #include <cooperative_groups.h>
 #include <type_traits>
 
@@ -586,13 +587,18 @@ ln_backward_kernel(const T* dy, const T* x, const W* weight, const float* mean, 
         in.take(f, st);
         F2(&u)[P] = f[0];
         F2(&xh)[P] = f[1];
-        const float scale = st[1], shift = -st[0] * st[1];
-        // columns behind the row: dy is 0 there, so whatever xh holds (finite) adds nothing
+        // Centred before it is scaled: x - mean is exact where they are close, so a mean far from zero
+        // costs no digits. Columns behind the row: x and dy read as 0 there, so what xh holds adds nothing
+        // as long as it is finite. (0 - mean) rstd is not where the product overflows; the elements of a
+        // row with such statistics are all its mean (the next fp32 value would be 10^31 deviations away),
+        // so there xh is 0 throughout.
+        const float scale = st[1], minus = -st[0];
+        const float scale_x = fabsf(minus * scale) <= FLT_MAX ? scale : 0.f;
         F2 s0 = F2(0.f, 0.f), s1 = s0;
         if (r < rows) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                xh[i] = fma2(xh[i], F2(scale, scale), F2(shift, shift));
+                xh[i] = mul2(add2(xh[i], F2(minus, minus)), F2(scale_x, scale_x));
                 dw[i] = fma2(u[i], xh[i], dw[i]);
                 db[i] = add2(db[i], u[i]);
                 u[i] = mul2(u[i], w[i]);

@@ -1,4 +1,5 @@
-"""Layer norm on the GPU beyond test_layer_norm_gpu.py: the sum without a residual through the C ABI."""
+"""Layer norm on the GPU beyond test_layer_norm_gpu.py: the sum without a residual through the C ABI, and the
+backward of rows whose mean is far from zero."""
 import ctypes
 
 import pytest
@@ -37,3 +38,44 @@ def test_sum_without_residual_is_x(cuda_lib, rows, D, dtype):
     a, z = x.clone(), torch.full_like(x, 7.0)
     assert abi_forward(cuda_lib, a, z, a) == 0
     assert torch.equal(a, x) and torch.equal(z, y)
+
+
+# ---------------------------------------------------------------- the backward's centred values
+
+def centred_check(ret, dy, x, w, mean, rstd, dsum, dtype, wdtype):
+    """The bounds of plain64 with x - mean for x and 0 for the mean: xh is then held to roundings of itself (the
+    difference and the product with rstd), whatever the mean's size."""
+    got = ret.layer_norm_backward(dy, x, w, mean, rstd, dsum=dsum)
+    c, zero = P.f64(x) - P.f64(mean)[:, None], torch.zeros_like(mean)
+    want = P.layer_norm_backward(dy, c, w, zero, rstd, dsum)
+    bounds = P.layer_norm_backward_bounds(dy, c, w, zero, rstd, dsum, dtype, wdtype, min(len(x), 1300))
+    for name, g, ref, bound in zip(("dx", "dweight", "dbias"), got, want, bounds):
+        P.assert_within(g, ref, bound, name)
+    return got
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("rows,D", [(5, 128), (40, 99), (7, 500), (4, 1023), (300, 771), (3, 4096), (3, 8191), (2, 12288),
+                                    (3, 9361), (2, 20000)])
+def test_backward_with_a_mean_far_from_zero(cuda_lib, rows, D, dtype, residual):
+    x, w = randn(rows, D, dtype=dtype, shift=1000.0), 1 + 0.3 * randn(D, seed=1)
+    dy = randn(rows, D, dtype=dtype, seed=2)
+    dsum = randn(rows, D, dtype=dtype, seed=3) if residual else None
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    cuda_lib.layer_norm(x, w, mean=mean, rstd=rstd)
+    centred_check(cuda_lib, dy, x, w, mean, rstd, dsum, dtype, f32)
+
+
+@pytest.mark.parametrize("dtype", [bf, f32])
+@pytest.mark.parametrize("D", [3, 40, 100, 259, 771, 4100, 8191, 9361, 20000])
+def test_backward_of_constant_rows(cuda_lib, D, dtype):
+    """x - mean is 0 exactly: no gradient of the weight, however large the constant (columns behind the row too
+    must stay out of the sums: there x reads as 0, and (0 - 1e37) / sqrt(eps) is not finite)."""
+    rows = 6
+    for value in (1000.0, 1e37):
+        x = torch.full((rows, D), value, device=DEV).to(dtype)
+        mean, rstd = x[:, 0].float().contiguous(), torch.full((rows,), EPS ** -0.5, device=DEV)
+        dy, w = randn(rows, D, dtype=dtype, seed=2), 1 + 0.3 * randn(D, seed=1)
+        _, dw, _ = centred_check(cuda_lib, dy, x, w, mean, rstd, None, dtype, f32)
+        assert not dw.any()
