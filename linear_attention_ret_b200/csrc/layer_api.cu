@@ -542,6 +542,8 @@ ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, co
     if (!q || !q_out || !q_strides || !q_out_strides || (rot > 0 && !freqs)) return RET_ERR_NULL;
     if (Hk > 0 && (!k || !k_out || !k_strides || !k_out_strides)) return RET_ERR_NULL;
     if (positions && starts) return RET_ERR_UNSUPPORTED;
+    if (rot > 0 && !aligned_to(freqs, 8)) return RET_ERR_ALIGN;
+    if (!aligned_to(positions, 8) || !aligned_to(starts, 8)) return RET_ERR_ALIGN;
     const size_t elt = elt_size(dt);
     RotArgs a{};
     Strided in[2], out[2];
