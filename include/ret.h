@@ -285,8 +285,8 @@ RET_API ret_status ret_msr_norm_gate(const void* o, const void* gate, void* y, i
  * o and dout [B, H, N, dv]; dy, gate and dgate token-major [B, N, H, dv]; all of dtype dt,
  * sums fp32. One pass: each input is read once and each gradient written once. dout may be
  * the o buffer, and dgate the gate or the dy buffer (in place); any other overlap of an
- * output is rejected with RET_ERR_UNSUPPORTED. Other errors as ret_msr_norm_gate, and
- * RET_ERR_ALIGN for a pointer that is not aligned to its element.
+ * output is rejected with RET_ERR_UNSUPPORTED, and so is dv above 2^29. Other errors as
+ * ret_msr_norm_gate, and RET_ERR_ALIGN for a pointer that is not aligned to its element.
  */
 RET_API ret_status ret_msr_norm_gate_backward(const void* dy, const void* o, const void* gate, void* dout, void* dgate,
                                               int B, int H, int N, int dv, float eps, ret_dtype dt, void* stream);
@@ -319,7 +319,7 @@ typedef enum {
  * (same address and strides); an output that is not seen to be disjoint from the other
  * tensors, or that writes an element twice, is rejected with RET_ERR_UNSUPPORTED. Column
  * blocks of one row-strided buffer (same strides, heads at distinct places of a row) count as
- * disjoint. RET_ERR_SHAPE: invalid sizes, rot odd or above d, a negative stride, a scale that
+ * disjoint. d above 2^29 is rejected likewise. RET_ERR_SHAPE: invalid sizes, rot odd or above d, a negative stride, a scale that
  * is not finite. RET_ERR_ALIGN: a pointer not aligned to its element.
  */
 RET_API ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, const long long* q_strides,
@@ -339,8 +339,8 @@ RET_API ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k
  *   mean, rstd    [rows] fp32, the row statistics for the backward pass, or NULL.
  * Statistics are fp32, of centred values, and with a residual of the unrounded sum. y and
  * sum_out may each be the x or the residual buffer (in place); other overlaps of an output
- * are rejected with RET_ERR_UNSUPPORTED. eps >= 0. rows = 0: nothing to do. RET_ERR_ALIGN: a pointer not
- * aligned to its element.
+ * are rejected with RET_ERR_UNSUPPORTED, and so is D above 2^29. eps >= 0. rows = 0: nothing to do.
+ * RET_ERR_ALIGN: a pointer not aligned to its element.
  */
 RET_API ret_status ret_layer_norm(const void* x, const void* residual, const void* weight, const void* bias, void* y,
                                   void* sum_out, float* mean, float* rstd, long long rows, int D, float eps,
@@ -354,7 +354,7 @@ RET_API ret_status ret_layer_norm(const void* x, const void* residual, const voi
  * of x and of residual alike. dsum [rows, D]: the gradient that reaches sum_out by other ways, or NULL.
  * dweight and dbias [D] of type wdt, each or both NULL; weight may be NULL (1). The sums over
  * rows are fp32 and in a fixed order: calls with the same sizes on the same device agree bit for bit. dx may be the
- * dy, x or dsum buffer (in place); other overlaps of an output are rejected with
+ * dy, x or dsum buffer (in place); other overlaps of an output, and D above 2^29, are rejected with
  * RET_ERR_UNSUPPORTED. May take stream-ordered scratch, freed on `stream` before the call
  * returns. rows = 0: dweight and dbias receive zeros.
  */

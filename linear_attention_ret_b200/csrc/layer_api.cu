@@ -96,6 +96,9 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, s
 
 // Most elements of one tensor: more than any device holds, few enough that byte counts fit.
 constexpr long long kMaxElements = 1LL << 46;
+// Longest row (layer norm's D, a head's d or dv): column numbers, a step of the general kernels' loops past
+// the last one, and a row of both column sums (2 D floats) are counted in 31 bits.
+constexpr int kMaxRow = 1 << 29;
 inline size_t elt_size(ret_dtype dt) { return dt == RET_BF16 ? 2 : 4; }
 inline bool valid_dtype(int dt) { return dt == RET_F32 || dt == RET_BF16; }
 
@@ -514,6 +517,7 @@ ret_status ret_msr_norm_gate_backward(const void* dy, const void* o, const void*
     if (!valid_dtype(dt)) return RET_ERR_DTYPE;
     if (B <= 0 || H <= 0 || N < 0 || dv <= 0) return RET_ERR_SHAPE;
     if (!(eps >= 0.f) || !std::isfinite(eps)) return RET_ERR_SHAPE;
+    if (dv > kMaxRow || (__int128)B * H * N > kMaxElements / dv) return RET_ERR_UNSUPPORTED;
     if (N == 0) return RET_OK;
     if (!dy || !o || !gate || !dout || !dgate) return RET_ERR_NULL;
     const size_t bytes = (size_t)B * H * N * dv * elt_size(dt);
@@ -538,6 +542,7 @@ ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, co
     if (B <= 0 || N < 0 || Hq <= 0 || Hk < 0 || d <= 0 || rot < 0 || rot > d || rot % 2 != 0) return RET_ERR_SHAPE;
     if (!std::isfinite(amplitude) || !std::isfinite(q_scale) || !std::isfinite(k_scale)) return RET_ERR_SHAPE;
     if (layout != RET_ROTARY_INTERLEAVED && layout != RET_ROTARY_HALF) return RET_ERR_UNSUPPORTED;
+    if (d > kMaxRow) return RET_ERR_UNSUPPORTED;
     if (N == 0) return RET_OK;
     if (!q || !q_out || !q_strides || !q_out_strides || (rot > 0 && !freqs)) return RET_ERR_NULL;
     if (Hk > 0 && (!k || !k_out || !k_strides || !k_out_strides)) return RET_ERR_NULL;
@@ -599,7 +604,7 @@ ret_status ret_layer_norm(const void* x, const void* residual, const void* weigh
     if (!valid_dtype(dt) || !valid_dtype(wdt)) return RET_ERR_DTYPE;
     if (wdt != dt && wdt != RET_F32) return RET_ERR_DTYPE;
     if (rows < 0 || D <= 0) return RET_ERR_SHAPE;
-    if (rows > kMaxElements / D) return RET_ERR_UNSUPPORTED;
+    if (D > kMaxRow || rows > kMaxElements / D) return RET_ERR_UNSUPPORTED;
     if (!(eps >= 0.f) || !std::isfinite(eps)) return RET_ERR_SHAPE;
     if (rows == 0) return RET_OK;
     if (!x || !y) return RET_ERR_NULL;
@@ -637,7 +642,7 @@ ret_status ret_layer_norm_backward(const void* dy, const void* x, const void* we
     if (!valid_dtype(dt) || !valid_dtype(wdt)) return RET_ERR_DTYPE;
     if (wdt != dt && wdt != RET_F32) return RET_ERR_DTYPE;
     if (rows < 0 || D <= 0) return RET_ERR_SHAPE;
-    if (rows > kMaxElements / D) return RET_ERR_UNSUPPORTED;
+    if (D > kMaxRow || rows > kMaxElements / D) return RET_ERR_UNSUPPORTED;
     cudaStream_t st = as_stream(stream);
     const size_t elt = elt_size(dt), welt = elt_size(wdt);
     const size_t bytes = (size_t)rows * D * elt, wb = (size_t)D * welt, sb = (size_t)rows * 4;
