@@ -9,10 +9,12 @@ Names match the C ABI: ret_parallel, ret_chunkwise, ret_recurrent_step,
 gated_ret_chunkwise. Tensors are CUDA, contiguous, heads leading:
 q, k [B, H, N, dk]; v [B, H, N, dv]; gamma [H] fp32; g [B, H, N] fp32;
 state [B, H, dk, dv] fp32. q, k, v share one dtype (float32 or bfloat16).
+A call on device tensors is made on their device, whichever is current.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -144,6 +146,20 @@ def _cuda(*ts):
             raise ValueError(f"tensors must be on one device, got {dev} and {t.device}")
 
 
+def _on_device_of_tensors(fn):
+    """A call whose first argument is a device tensor, made with that tensor's device current: the library launches
+    on the current device, where another device's addresses are not valid."""
+    @functools.wraps(fn)
+    def call(*args, **kwargs):
+        t = args[0] if args else next(iter(kwargs.values()), None)
+        index = t.get_device() if hasattr(t, "get_device") else -1
+        if index >= 0 and index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
+    return call
+
+
 def _host(*ts):
     for t in ts:
         if t.is_cuda or not t.is_contiguous():
@@ -196,6 +212,7 @@ def _step_args(q, k, v, decay, state, o, gated):
     return B, H, dk, dv
 
 
+@_on_device_of_tensors
 def ret_parallel(q, k, v, gamma, o=None, stream=None):
     """O = (Q K^T (.) D) V. Returns o [B, H, N, dv] (dtype of q)."""
     B, H, N, dk, dv = _seq_args(q, k, v, gamma, False, o)
@@ -206,6 +223,7 @@ def ret_parallel(q, k, v, gamma, o=None, stream=None):
     return o
 
 
+@_on_device_of_tensors
 def ret_chunkwise(q, k, v, gamma, chunk, state_in=None, state_out=None, o=None, stream=None):
     """Chunkwise retention. Returns o; writes the final state into state_out if given."""
     B, H, N, dk, dv = _seq_args(q, k, v, gamma, False, o, state_in, state_out)
@@ -217,6 +235,7 @@ def ret_chunkwise(q, k, v, gamma, chunk, state_in=None, state_out=None, o=None, 
     return o
 
 
+@_on_device_of_tensors
 def ret_chunkwise_noalloc(q, k, v, gamma, chunk, state_in=None, state_out=None, o=None, stream=None):
     """ret_chunkwise without device allocation by the library: scratch comes from a
     fixed 16 MiB buffer inside libret.so (see include/ret.h). Returns o."""
@@ -229,6 +248,7 @@ def ret_chunkwise_noalloc(q, k, v, gamma, chunk, state_in=None, state_out=None, 
     return o
 
 
+@_on_device_of_tensors
 def gated_ret_chunkwise(q, k, v, g, chunk, state_in=None, state_out=None, o=None, stream=None):
     """Gated chunkwise retention (per-token log-decay g). Returns o."""
     B, H, N, dk, dv = _seq_args(q, k, v, g, True, o, state_in, state_out)
@@ -265,6 +285,7 @@ def gated_ret_chunkwise_host(q, k, v, g, chunk, o=None, stream=None, sync=True):
     return _chunkwise_host("gated_ret_chunkwise_host", q, k, v, g, chunk, o, True, stream, sync)
 
 
+@_on_device_of_tensors
 def ret_recurrent_step(q, k, v, gamma, state, o=None, stream=None):
     """One decode step; updates state [B, H, dk, dv] in place and returns o [B, H, dv]."""
     B, H, dk, dv = _step_args(q, k, v, gamma, state, o, False)
@@ -275,6 +296,7 @@ def ret_recurrent_step(q, k, v, gamma, state, o=None, stream=None):
     return o
 
 
+@_on_device_of_tensors
 def gated_ret_recurrent_step(q, k, v, g, state, o=None, stream=None):
     """One gated decode step with log-decay g [B, H] (fp32); updates state in place, returns o [B, H, dv]."""
     B, H, dk, dv = _step_args(q, k, v, g, state, o, True)
@@ -286,6 +308,7 @@ def gated_ret_recurrent_step(q, k, v, g, state, o=None, stream=None):
     return o
 
 
+@_on_device_of_tensors
 def chunkwise_state(k, v, decay, chunk, gated=False, state_out=None, log2_decay=None, stream=None):
     """End state U [B, H, dk, dv] of a segment from a zero start and log2 of its total decay
     [B, H] (decay: gamma [H], or g [B, H, N] with gated=True). Returns (U, log2_decay)."""
@@ -300,6 +323,7 @@ def chunkwise_state(k, v, decay, chunk, gated=False, state_out=None, log2_decay=
     return state_out, log2_decay
 
 
+@_on_device_of_tensors
 def state_prefix(seg_states, seg_log2_decay, state_in=None, stream=None):
     """Start states [R, B, H, dk, dv] of R consecutive segments and the state after all of
     them, from their end states U [R, B, H, dk, dv] and log2 decays [R, B, H]."""
@@ -316,6 +340,7 @@ def state_prefix(seg_states, seg_log2_decay, state_in=None, stream=None):
     return starts, end
 
 
+@_on_device_of_tensors
 def chunkwise_backward(q, k, v, decay, dout, chunk, gated=False, ddecay=True, stream=None):
     """Gradients of sum(dout * o) for o = ret_chunkwise(q, k, v, decay) (gated=True:
     gated_ret_chunkwise with g = decay) from a zero initial state. Returns
@@ -365,6 +390,7 @@ def chunkwise_backward_host(q, k, v, decay, dout, chunk, gated=False, ddecay=Tru
     return dq, dkk, dvv, dd
 
 
+@_on_device_of_tensors
 def msr_norm_gate(o, gate, eps: float = 1e-5, y=None, stream=None):
     """Multi-scale retention output epilogue: y[b, n, h] = swish(gate[b, n, h]) * RMSNorm(o[b, h, n])
     over dv (no affine weights). o [B, H, N, dv]; gate [B, N, H, dv] (same dtype);

@@ -1,4 +1,8 @@
-"""Refusals of the operators around retention beyond test_operators_host.py: nothing is launched."""
+"""Refusals of the operators around retention beyond test_operators_host.py, and the device that calls enter:
+nothing is launched."""
+import torch
+
+from linear_attention_ret_b200 import ret
 from tests.test_operators_host import ALIGN, BASE, UNSUPPORTED, _rot, lib, p  # noqa: F401 - lib is a fixture
 
 
@@ -31,3 +35,41 @@ def test_more_elements_than_a_byte_count_holds(lib):
     big = (1 << 31) - 1
     assert lib.ret_msr_norm_gate_backward(p(far), p(2 * far), p(3 * far), p(4 * far), p(5 * far), big, big, big, 64,
                                           1e-5, 1, None) == UNSUPPORTED
+
+
+# ---------------------------------------------------------------- the path's calls on another device
+
+class _Tensor:
+    """Of a tensor, what a call asks before it enters the tensor's device."""
+
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+
+def test_every_call_on_device_tensors_enters_their_device(monkeypatch):
+    entered = []
+
+    class Entered:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            entered.append(self.index)
+
+        def __exit__(self, *_):
+            entered.append("left")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", Entered)
+    call = ret._on_device_of_tensors(lambda *a, **k: list(entered))
+    assert call(_Tensor(0), 64) == []             # the current device: nothing to enter
+    assert call(_Tensor(-1), 64) == []            # a host tensor: refused later, by the call itself
+    assert call(_Tensor(1), 64) == [1] and entered == [1, "left"]
+    entered.clear()
+    assert call(q=_Tensor(2), chunk=64) == [2]
+    for name in ("ret_parallel", "ret_chunkwise", "ret_chunkwise_noalloc", "gated_ret_chunkwise", "ret_recurrent_step",
+                 "gated_ret_recurrent_step", "chunkwise_state", "state_prefix", "chunkwise_backward", "msr_norm_gate"):
+        assert hasattr(getattr(ret, name), "__wrapped__"), name
