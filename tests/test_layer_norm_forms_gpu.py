@@ -1,12 +1,12 @@
 """Layer norm on the GPU beyond test_layer_norm_gpu.py: the sum without a residual through the C ABI, and the
-backward of rows whose mean is far from zero."""
+backward of rows whose mean is far from zero, and sizes at which every block takes many rows."""
 import ctypes
 
 import pytest
 import torch
 
 from tests import plain64 as P
-from tests.test_layer_norm_gpu import DEV, EPS, bf, f32, randn
+from tests.test_layer_norm_gpu import DEV, EPS, backward_check, bf, f32, forward_check, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,27 @@ def test_backward_of_constant_rows(cuda_lib, D, dtype):
         dy, w = randn(rows, D, dtype=dtype, seed=2), 1 + 0.3 * randn(D, seed=1)
         _, dw, _ = centred_check(cuda_lib, dy, x, w, mean, rstd, None, dtype, f32)
         assert not dw.any()
+
+
+# ---------------------------------------------------------------- many rows per block
+
+# Blocks stay and take row after row: enough rows that every block goes round its slots in shared memory more
+# than once (two to four slots; up to sixteen small blocks per SM). Widths of one vector up to a pair of blocks.
+MANY = [(230000, 40), (60000, 99), (60000, 100), (12000, 771), (9189, 1023), (12000, 1024), (4000, 2050), (3000, 4096),
+        (3000, 6001), (700, 9361), (1000, 16384)]
+
+
+@pytest.fixture
+def plain_on_device(monkeypatch):
+    """The plain 64-bit forms where the tensors are: these cases are large."""
+    monkeypatch.setattr(P, "f64", lambda t: None if t is None else t.detach().double())
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(bf, f32), (f32, f32)], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("rows,D", MANY)
+def test_many_rows_per_block(cuda_lib, plain_on_device, rows, D, dtype, wdtype):
+    forward_check(cuda_lib, rows, D, dtype, wdtype, residual=True, seed=10)
+    backward_check(cuda_lib, rows, D, dtype, wdtype)
+    dy, x, w, mean, rstd, dsum, got = backward_check(cuda_lib, rows, D, dtype, wdtype, residual=True, seed=20)
+    again = cuda_lib.layer_norm_backward(dy, x, w, mean, rstd, dsum=dsum)
+    assert all(torch.equal(a, g) for a, g in zip(again, got))
