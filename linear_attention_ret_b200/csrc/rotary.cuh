@@ -55,7 +55,7 @@ __device__ __forceinline__ void rot_angle(const RotArgs& a, long long p, int i, 
 // two vectors, those whose elements pair up or two neighbours behind the rotated part. With VE = 1
 // (odd sizes and alignments) a unit is two elements in either layout. Threads of neighbouring
 // units and heads lie side by side, so a warp reads whole stretches of a token-major row. A block
-// holds `tokens` tokens of `split` head groups of q and of k each. With fewer heads than BATCH
+// holds `tokens` tokens of `split` head groups of q and of k each. With one or two heads
 // (MANY) each has its thread, and the thread's rows are of BATCH tokens, `at_once` apart: BATCH rows
 // are in flight either way, and what a block costs once is spread over as many.
 // cos and sin of a token are formed once per block, in shared memory, and serve all heads of q and
