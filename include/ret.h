@@ -319,8 +319,8 @@ typedef enum {
  * (same address and strides); an output that is not seen to be disjoint from the other
  * tensors, or that writes an element twice, is rejected with RET_ERR_UNSUPPORTED. Column
  * blocks of one row-strided buffer (same strides, heads at distinct places of a row) count as
- * disjoint. d above 2^29 is rejected likewise. RET_ERR_SHAPE: invalid sizes, rot odd or above d, a negative stride, a scale that
- * is not finite. RET_ERR_ALIGN: a pointer not aligned to its element.
+ * disjoint. d above 2^29 is rejected likewise. RET_ERR_SHAPE: invalid sizes, rot odd or above d, a
+ * negative stride, a scale that is not finite. RET_ERR_ALIGN: a pointer not aligned to its element.
  */
 RET_API ret_status ret_rotary(const void* q, const void* k, void* q_out, void* k_out, const long long* q_strides,
                               const long long* k_strides, const long long* q_out_strides,
@@ -353,9 +353,9 @@ RET_API ret_status ret_layer_norm(const void* x, const void* residual, const voi
  * x is the normalised input: with a residual the forward's sum_out, and dx is then the gradient
  * of x and of residual alike. dsum [rows, D]: the gradient that reaches sum_out by other ways, or NULL.
  * dweight and dbias [D] of type wdt, each or both NULL; weight may be NULL (1). The sums over
- * rows are fp32 and in a fixed order: calls with the same sizes on the same device agree bit for bit. dx may be the
- * dy, x or dsum buffer (in place); other overlaps of an output, and D above 2^29, are rejected with
- * RET_ERR_UNSUPPORTED. May take stream-ordered scratch, freed on `stream` before the call
+ * rows are fp32 and in an order that sizes, types, the pointers' alignment and whether dsum is given fix: calls that
+ * agree in these on the same device agree bit for bit. dx may be the dy, x or dsum buffer (in place); other overlaps
+ * of an output, and D above 2^29, are rejected with RET_ERR_UNSUPPORTED. May take stream-ordered scratch, freed on `stream` before the call
  * returns. rows = 0: dweight and dbias receive zeros.
  */
 RET_API ret_status ret_layer_norm_backward(const void* dy, const void* x, const void* weight, const float* mean,

@@ -96,7 +96,9 @@ class MsrNormGate(torch.autograd.Function):
 
 
 def msr_norm_gate(o, gate, eps: float = 1e-5):
-    """Differentiable ret.msr_norm_gate: o [B, H, N, dv], gate [B, N, H, dv], y [B, N, H, dv]."""
+    """Differentiable ret.msr_norm_gate: o [B, H, N, dv], gate [B, N, H, dv], y [B, N, H, dv]. The kernel takes
+    contiguous tensors: a gate that is a slice of a fused projection is copied first, and the copy kept for the
+    backward."""
     return MsrNormGate.apply(o, gate, eps)
 
 
@@ -138,8 +140,9 @@ def multi_scale_retention(q, k, v, gate, decay, freqs=None, chunk: int = 64, gat
                           positions=None, starts=None, offset=0, layout="interleaved", amplitude=1.0, q_scale=1.0,
                           k_scale=1.0):
     """RetNet's multi-scale retention between its projections, differentiable: q, k [B, N, H, dk], v and gate
-    [B, N, H, dv] token-major (slices of a fused projection too), decay gamma [H] or g [B, H, N]; returns
-    [B, N, H, dv] for the output projection. Rotary prologue, chunkwise retention, norm and gate."""
+    [B, N, H, dv] token-major (slices of a fused projection too; q, k and v are read in place, such a gate is copied),
+    decay gamma [H] or g [B, H, N]; returns [B, N, H, dv] for the output projection. Rotary prologue, chunkwise
+    retention, norm and gate."""
     qh, kh = rotary(q, k, freqs, positions, starts, offset, layout, amplitude, q_scale, k_scale)
     vh, _ = rotary(v, None, None)  # layout only
     return msr_norm_gate(chunkwise_retention(qh, kh, vh, decay, chunk, gated), gate, eps)

@@ -207,7 +207,7 @@ ret_status launch_rotary_vec(const RotArgs& a, int apart, cudaStream_t st) {
     if (heads < 3 && heads * units <= kRotThreads &&
         (long long)a.B * a.N >= (long long)4 * (kRotThreads / (heads * units)) * 2 * sm_count())
         return launch_rotary_batch<T, VE, HALF, 4, true>(a, apart, st);
-    // Eight rows at once from eight heads on, whole batches: 134 MB, half layout, twelve heads of 128 23.9 us against
+    // Eight rows at once from eight heads on: 134 MB, half layout, twelve heads of 128 23.9 us against
     // 25.5 us with four rows, eight and sixteen heads within 2% (six heads of 256 would take it too: 24.1 against 25.6).
     if constexpr (HALF && VE > 1 && VE * sizeof(T) <= 8)
         if (heads >= 8) return launch_rotary_batch<T, VE, HALF, 8, false>(a, apart, st);

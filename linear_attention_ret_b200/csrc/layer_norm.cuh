@@ -422,8 +422,10 @@ struct RowSpan {
 // Single elements are read through spans where that was faster: the forward of fp32 (9189 x 1023 with a
 // residual: 27.5 us against 32.2 us), the backward of fp32 with three tensors (16400 x 1023: 51.2 us
 // against 61.9 us; with two 55.7 us against 51.2 us) and, of either type, the backward's rows above 4,096
-// elements (2048 x 8191 in bf16: 38.6 us against 62.7 us). Elsewhere bf16 waits in registers (16400 x
-// 1023: forward 26.8 us against 30.8 us, backward 33.4 us against 55.5 us).
+// elements (2048 x 8191 in bf16: 38.9 us against 62.7 us). Elsewhere bf16 waits in registers (forward of
+// 16400 x 1023 26.8 us against 30.8 us, of 2048 x 8191 30.6 against 32.7 and of 1365 x 12289 53.9 against
+// 62.9, with a residual 34.2 against 34.6, 43.6 against 41.7 and 73.9 against 106; backward of 16400 x 1023
+// 33.4 us against 55.5 us). The backward's widest form by spans with three tensors spills 80 to 104 bytes.
 template <typename T, int VE, int EPT, int N, int N_STAT>
 constexpr bool by_span() {
     if (VE > 1) return false;
@@ -712,7 +714,8 @@ ln_forward_rows_kernel(const T* x, const T* res, const W* __restrict__ weight, c
     }
 }
 
-// dx of any D: one block per row, two passes.
+// dx of any D: one block per row, two passes. This kernel, the one above and the one below are ordinary
+// launches and have no wait for the kernel before them: __restrict__ is safe in them for that reason alone.
 template <typename T, typename W>
 __global__ void __launch_bounds__(kLnThreads)
 ln_backward_rows_kernel(const T* dy, const T* x, const W* __restrict__ weight, const float* __restrict__ mean,
@@ -755,7 +758,7 @@ ln_backward_columns_kernel(const T* __restrict__ dy, const T* __restrict__ x, co
 }
 
 // dw and db from `parts` rows of partial sums: 16 columns per block, four per thread, 64 threads per
-// column over every 64th row; those are joined in a fixed order, so calls agree bit for bit.
+// column over every 64th row; those are joined in a fixed order, so equal calls agree bit for bit.
 constexpr int kReduceColumns = 16, kReduceQuads = kReduceColumns / 4;
 template <typename W>
 __global__ void __launch_bounds__(kLnThreads)

@@ -27,8 +27,9 @@ __device__ __forceinline__ float sigmoid(float x) {
 // read by the thread that writes it.
 //
 // Blocks per SM: left alone, the two-vector form (dv = 512) keeps the first pass's unpacked
-// values, 93 registers and two blocks: 60.2 us at the 1.3B-shaped output (336 MB), 55.3 us with three
-// blocks (6.07 TB/s), 59.8 us with four, which spill.
+// values, 93 registers and two blocks: 60.2 us at the 1.3B-shaped output (336 MB), 54.8 us with three
+// blocks (6.13 TB/s; 80 registers, 16 bytes spilled), 59.8 us with four, which spill more. Longer bf16 rows
+// spill 80 to 92 bytes at their one or two blocks.
 template <typename T, int VE, int LPR, int CH>
 __global__ void __launch_bounds__(kNormThreads, VE * CH * sizeof(T) <= 32 ? 3 : VE * CH * sizeof(T) <= 64 ? 2 : 1)
 norm_gate_backward_vec_kernel(const T* dy, const T* o, const T* gate, T* dout, T* dgate, FastDiv H, FastDiv N, int dv,
@@ -99,7 +100,9 @@ norm_gate_backward_vec_kernel(const T* dy, const T* o, const T* gate, T* dout, T
     }
 }
 
-// Any dv and alignment: one warp per row, two passes over the row (the second from L1/L2).
+// Any dv and alignment: one warp per row, two passes over the row (the second from L1/L2). An
+// ordinary launch: it has no wait for the kernel before it (likewise the general kernels of the other
+// operators around retention).
 // dgate may be gate or dy, and dout o: an element is read by the thread that writes it.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads)

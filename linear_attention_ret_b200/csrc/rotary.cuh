@@ -115,6 +115,8 @@ struct RotUnit {
 // registers and leave three blocks on an SM instead of four (134 MB, 4 heads of 128: 26.9 us against
 // 25.9 us), and with eight heads or more a thread takes eight rows at once (gradient at the gated
 // layer's shapes, 268 MB: 47.0 us with four, 44.6 us with eight, 6.0 TB/s; the interleaved layout gains nothing).
+// fp32 keeps 16-byte vectors in both layouts: 268 MB, 4 heads of 128 42.5 us interleaved (6.3 TB/s) and
+// 44.2 us half (6.1 TB/s), although the half layout's four rows of two vectors spill 48 bytes at 64 registers.
 template <typename T, int VE, bool HALF, int BATCH, bool MANY>
 __global__ void __launch_bounds__(kRotThreads, BATCH > 4 ? 3 : 4) rotary_vec_kernel(const RotArgs a, const RotPlan pl) {
     using Unit = RotUnit<T, VE, HALF, BATCH>;
@@ -204,7 +206,8 @@ __global__ void __launch_bounds__(kRotThreads, BATCH > 4 ? 3 : 4) rotary_vec_ker
     }
 }
 
-// Any width and alignment. One thread per pair, or element behind the rotated part, of q and k.
+// Any width and alignment. One thread per pair, or element behind the rotated part, of q and k. An
+// ordinary launch: it has no wait for the kernel before it.
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotArgs a, size_t total) {
     const int units = a.d - a.rot / 2, H = a.x[0].H + a.x[1].H;

@@ -10,8 +10,8 @@ pytestmark = pytest.mark.gpu
 
 KW = dict(q_scale=0.75, amplitude=1.1, offset=3)
 
-# B, N, Hq, Hk, d, rot: fewer than four heads and more tokens than 4 (256 / (heads x units)) blocks of two per SM
-# take, no whole number of blocks
+# B, N, Hq, Hk, d, rot: one to three heads and more tokens than two blocks per SM of 4 (256 / (heads x units))
+# tokens each take, no whole number of blocks
 FEW_HEADS = [
     (1, 9475, 1, 1, 128, 128),
     (2, 4801, 2, 2, 64, 64),
@@ -22,6 +22,7 @@ FEW_HEADS = [
     (1, 1203, 3, 3, 256, 256),
     (1, 37891, 1, 1, 32, 32),
     (1, 9501, 1, 2, 100, 50),   # pairs of bf16
+    (1, 14301, 1, 2, 40, 24),
 ]
 
 # heads of more units than a block has threads, for q and k together
