@@ -541,7 +541,7 @@ __host__ __device__ constexpr int ln_pitch(int D) { return (D + 3) / 4 * 4; }
 // every row it takes, their dw and db sums in registers; the next rows are in flight. Groups of
 // whole warps share a block of 512 threads, one row each, and join their column sums at the end:
 // each block leaves one row of partial sums, part [blocks, 2, ln_pitch(D)], which ln_reduce_kernel
-// adds in order. HBM-bound: 8192 x 4096 in bf16 with the sum's gradient (269 MB) 48.4 us with the
+// adds in order. HBM-bound: 8192 x 4096 in bf16 with the sum's gradient (269 MB) 48.9 us with the
 // reduction, 5.5 TB/s; dx and the column sums in a pass each took 228 us. Joining partial sums over
 // clusters instead was slower (8192 x 2048: 38.4 us against 27.7 us).
 // PAIR: rows too wide for the registers of one block are split over the two blocks of a cluster, each
