@@ -355,8 +355,8 @@ RET_API ret_status ret_layer_norm(const void* x, const void* residual, const voi
  * dweight and dbias [D] of type wdt, each or both NULL; weight may be NULL (1). The sums over
  * rows are fp32 and in an order that sizes, types, the pointers' alignment and whether dsum is given fix: calls that
  * agree in these on the same device agree bit for bit. dx may be the dy, x or dsum buffer (in place); other overlaps
- * of an output, and D above 2^29, are rejected with RET_ERR_UNSUPPORTED. May take stream-ordered scratch, freed on `stream` before the call
- * returns. rows = 0: dweight and dbias receive zeros.
+ * of an output, and D above 2^29, are rejected with RET_ERR_UNSUPPORTED. May take stream-ordered scratch, freed on
+ * `stream` before the call returns. rows = 0: dweight and dbias receive zeros.
  */
 RET_API ret_status ret_layer_norm_backward(const void* dy, const void* x, const void* weight, const float* mean,
                                            const float* rstd, const void* dsum, void* dx, void* dweight, void* dbias,
